@@ -1,18 +1,20 @@
 // C ABI of libsas (declared in include/sas.h): argument validation, workspace
 // carving and kernel launches. Host code only; the kernels live in k_*.cu.
-#include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 
 #include <string>
 
 #include "../../include/sas.h"
+#include "api_common.h"
 #include "kernels.h"
 #include "ptx.cuh"
 
-namespace {
+namespace sas {
 
-thread_local std::string g_last_error;
+static thread_local std::string g_last_error;
+
+void clear_error() { g_last_error.clear(); }
 
 sas_status fail(sas_status s, const char* fmt, ...) {
   char buf[512];
@@ -29,19 +31,6 @@ sas_status cuda_status(cudaError_t e, const char* where) {
   return fail(SAS_ERR_CUDA, "%s: %s", where, cudaGetErrorString(e));
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-#define REQUIRE(cond, st, ...) \
-  do {                         \
-    if (!(cond)) return fail(st, __VA_ARGS__); \
-  } while (0)
-
-#define REQUIRE_PTR(p)                                                                   \
-  do {                                                                                   \
-    if ((p) == nullptr) return fail(SAS_ERR_INVALID_ARG, "%s must not be NULL", #p);     \
-    if (!aligned16(p)) return fail(SAS_ERR_INVALID_ARG, "%s must be 16-byte aligned", #p); \
-  } while (0)
-
 sas_status check_common(sas_dtype dt, int B, int Hq, int Hkv, int N, int d, int topk) {
   REQUIRE(dt == SAS_F32 || dt == SAS_BF16, SAS_ERR_INVALID_ARG, "dtype must be SAS_F32 or SAS_BF16");
   REQUIRE(B >= 0 && N >= 0, SAS_ERR_INVALID_ARG, "B and N must be >= 0 (B=%d N=%d)", B, N);
@@ -54,11 +43,15 @@ sas_status check_common(sas_dtype dt, int B, int Hq, int Hkv, int N, int d, int 
   return SAS_OK;
 }
 
-float resolve_scale(float scale, int d) { return scale > 0.f ? scale : 1.0f / sqrtf((float)d); }
+}  // namespace sas
 
-size_t a16(size_t x) { return (x + 15) & ~(size_t)15; }
-
-}  // namespace
+using sas::a16;
+using sas::aligned16;
+using sas::check_common;
+using sas::cuda_status;
+using sas::fail;
+using sas::g_last_error;
+using sas::resolve_scale;
 
 extern "C" {
 
@@ -683,6 +676,12 @@ sas_status sas_device_status(int clear, sas_stream_t stream) {
       {"k_wait_selftest", sas::selftest_error_word},
       {"k_summary_last", sas::summary_error_word},
       {"k_attn_*_tokens", sas::tokens_error_word},
+      {"k_rotary", sas::rotary_error_word},
+      {"k_page_*", sas::pages_error_word},
+      {"k_append", sas::append_error_word},
+      {"k_tree_select", sas::tree_select_error_word},
+      {"k_tree_attn_simt", sas::tree_attn_error_word},
+      {"k_tree_attn_tc", sas::tree_tc_error_word},
   };
   cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_status(e, "sas_device_status synchronize");

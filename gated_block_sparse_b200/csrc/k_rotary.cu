@@ -1,0 +1,128 @@
+// Rotary positions of q and k, forward and backward, in one launch.
+//
+// A thread holds one unit (2 VN elements, VN pairs) of one token: it computes
+// the unit's VN sines and cosines once and applies them to that unit of every
+// head of its slice, of q and then of k. Memory bounds it: every element is
+// read once and written once.
+#include "common.cuh"
+#include "kernels.h"
+#include "ptx.cuh"
+#include "rotary.cuh"
+
+namespace sas {
+
+__device__ uint32_t g_rotary_err = 0;
+
+namespace {
+constexpr int RT_THREADS = 256;
+}
+
+// Depth of drafted token i: its number of ancestors. A parent is below its
+// child, so each hop goes down and the walk ends; any other entry is
+// reported and read as -1 (a child of the last cached token).
+__device__ __forceinline__ int draft_depth(const int32_t* __restrict__ parents, int i,
+                                           uint32_t* err) {
+  int n = 0;
+  while (true) {
+    const int p = __ldg(parents + i);
+    if (p < -1 || p >= i) {
+      atomicOr(err, kErrBadIndex);
+      return n;
+    }
+    if (p < 0) return n;
+    ++n;
+    i = p;
+  }
+}
+
+template <typename T, int VN>
+__global__ void __launch_bounds__(RT_THREADS) k_rotary(
+    RotaryTensor q, RotaryTensor k, int N, int d, const float* __restrict__ inv_freq, int rot,
+    int interleaved, float amp, int inverse, const int32_t* __restrict__ pos,
+    const int32_t* __restrict__ start, const int32_t* __restrict__ parents, int hslice) {
+  const int U = d / (2 * VN);
+  const long long item = (long long)blockIdx.x * RT_THREADS + threadIdx.x;
+  const int b = blockIdx.z;
+  const int n = (int)(item / U), u = (int)(item % U);
+  if (n >= N) return;
+  int p;
+  if (pos)
+    p = __ldg(pos + (size_t)b * N + n);
+  else
+    p = (start ? __ldg(start + b) : 0) +
+        (parents ? draft_depth(parents + (size_t)b * N, n, &g_rotary_err) : n);
+  const bool turned = u < rot / (2 * VN);
+  float c[VN], s[VN];
+  if (turned) unit_sincos<VN>(inv_freq, u, p, amp, inverse, c, s);
+  int e0, e1;
+  unit_offsets<VN>(u, rot, interleaved, e0, e1);
+  const int h0 = blockIdx.y * hslice, h1 = min(h0 + hslice, q.H + k.H);
+#pragma unroll 4
+  for (int h = h0; h < h1; ++h) {
+    const bool isq = h < q.H;
+    const RotaryTensor& t = isq ? q : k;
+    const int hh = isq ? h : h - q.H;
+    const T* x = static_cast<const T*>(t.x) + b * t.xs[0] + hh * t.xs[1] + n * t.xs[2];
+    T* y = static_cast<T*>(t.y) + b * t.ys[0] + hh * t.ys[1] + n * t.ys[2];
+    float a[VN], bb[VN];
+    load_vec<T, VN>(x + e0, a);
+    load_vec<T, VN>(x + e1, bb);
+    if (turned) rotate_unit<VN>(a, bb, c, s, interleaved);
+    store_vec<T, VN>(y + e0, a);
+    store_vec<T, VN>(y + e1, bb);
+  }
+}
+
+template <typename T, int VN>
+static cudaError_t launch(const RotaryTensor& q, const RotaryTensor& k, int B, int N, int d,
+                          const float* inv_freq, int rot, int interleaved, float amp, int inverse,
+                          const int32_t* pos, const int32_t* start, const int32_t* parents,
+                          cudaStream_t st) {
+  const long long items = (long long)N * (d / (2 * VN));
+  const long long blocks = (items + RT_THREADS - 1) / RT_THREADS;
+  const int H = q.H + k.H;
+  // heads per thread: as many as leave the grid about four blocks an SM
+  const long long want = 148 * 4;
+  long long slices = (want + blocks * B - 1) / (blocks * B);
+  if (slices < 1) slices = 1;
+  if (slices > H) slices = H;
+  const int hslice = (int)((H + slices - 1) / slices);
+  dim3 grid((unsigned)blocks, (H + hslice - 1) / hslice, B);
+  k_rotary<T, VN><<<grid, RT_THREADS, 0, st>>>(q, k, N, d, inv_freq, rot, interleaved, amp,
+                                               inverse, pos, start, parents, hslice);
+  return cudaGetLastError();
+}
+
+// Vectors fit when the rotated width and every stride are multiples of them
+// (the base pointers are 16-byte aligned by the interface).
+static bool strides_fit(const RotaryTensor& t, int vn) {
+  if (t.H == 0) return true;
+  for (int i = 0; i < 3; ++i)
+    if (t.xs[i] % vn || t.ys[i] % vn) return false;
+  return true;
+}
+
+cudaError_t launch_rotary(const RotaryTensor& q, const RotaryTensor& k, int bf16, int B, int N,
+                          int d, const float* inv_freq, int rot, int interleaved, float amp,
+                          int inverse, const int32_t* pos, const int32_t* start,
+                          const int32_t* parents, cudaStream_t st) {
+  const int vn = bf16 ? 8 : 4;
+  const bool vec = rot % (2 * vn) == 0 && strides_fit(q, vn) && strides_fit(k, vn);
+  if (bf16)
+    return vec ? launch<__nv_bfloat16, 8>(q, k, B, N, d, inv_freq, rot, interleaved, amp, inverse,
+                                          pos, start, parents, st)
+               : launch<__nv_bfloat16, 1>(q, k, B, N, d, inv_freq, rot, interleaved, amp, inverse,
+                                          pos, start, parents, st);
+  return vec ? launch<float, 4>(q, k, B, N, d, inv_freq, rot, interleaved, amp, inverse, pos,
+                                start, parents, st)
+             : launch<float, 1>(q, k, B, N, d, inv_freq, rot, interleaved, amp, inverse, pos,
+                                start, parents, st);
+}
+
+uint32_t* rotary_error_word() {
+  void* p = nullptr;
+  cudaGetSymbolAddress(&p, g_rotary_err);
+  return static_cast<uint32_t*>(p);
+}
+
+}  // namespace sas

@@ -1,0 +1,268 @@
+// Attention of drafted tokens over the selected blocks, the cache's tail and
+// their ancestors (fp32 caches), split over the units of a kv group, and the
+// join of the splits.
+//
+//   o_i = softmax(scale q_i K + bias) V over the kept blocks (bias log g),
+//   the tail and the path (bias 0, or log g of block c0 for the keys that a
+//   path has moved into it; left out when the token does not keep c0).
+//
+// k_tree_attn_simt: one CTA per (32 rows, kv group, split), rows being the
+// group's heads x drafted tokens. Every unit (64 keys) is read once per CTA;
+// a warp owns four rows and keeps their running maximum, sum and output in
+// registers. fp32 FMAs bound it.
+#include <math.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "ptx.cuh"
+#include "tree.cuh"
+
+namespace sas {
+
+__device__ uint32_t g_tree_attn_err = 0;
+
+namespace {
+constexpr int TA_THREADS = 256;
+constexpr int TA_ROWS = 32;  // rows of a CTA
+constexpr int TA_WROWS = TA_ROWS / (TA_THREADS / 32);
+constexpr float LOG2E = 1.4426950408889634f;
+}  // namespace
+
+template <int D>
+__global__ void __launch_bounds__(TA_THREADS) k_tree_attn_simt(TreeArgs a, TreeWs w) {
+  constexpr int LD = D + 4, E = D / 32;
+  extern __shared__ __align__(16) float sm_f[];
+  float* qs = sm_f;                 // [32][D]
+  float* ks = qs + TA_ROWS * D;     // [64][LD]
+  float* vs = ks + SAS_BLOCK * LD;  // [64][D]
+  uint32_t* bits = reinterpret_cast<uint32_t*>(vs + SAS_BLOCK * D);
+  __shared__ TreeShared tree;
+  __shared__ int warp_s[TA_THREADS / 32];
+  __shared__ int start_s;
+  const int r = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int split = blockIdx.x % a.ns, tile = blockIdx.x / a.ns;
+  const int G = a.Hq / a.Hkv;
+  const size_t group = (size_t)b * a.Hkv + r;
+  const TreeSeq s = tree_seq(a, b, nullptr);
+  const int rows = G * s.nt, row0 = tile * TA_ROWS;
+  if (row0 >= rows) return;
+  tree_masks(a, b, s.nt, tree, nullptr);
+  int u0, u1;
+  const int nu = tree_units<TA_THREADS>(a, w.ubits + group * a.words, bits, warp_s, &start_s,
+                                        split, u0, u1);
+  const unsigned long long early_tok = tree_early(tree, s);
+  const float* q = static_cast<const float*>(a.q);
+  for (int e = tid; e < TA_ROWS * D / 4; e += TA_THREADS) {
+    const int row = row0 + e / (D / 4), c = (e % (D / 4)) * 4;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (row < rows)
+      x = *reinterpret_cast<const float4*>(
+          q + (((size_t)b * a.Hq + r * G + row / s.nt) * a.T + row % s.nt) * D + c);
+    *reinterpret_cast<float4*>(qs + (e / (D / 4)) * D + c) = x;
+  }
+  float m[TA_WROWS], l[TA_WROWS], acc[TA_WROWS][E];
+  TreeRow info[TA_WROWS];
+  int tok[TA_WROWS];
+#pragma unroll
+  for (int i = 0; i < TA_WROWS; ++i) {
+    const int row = row0 + wid * TA_WROWS + i;
+    m[i] = -1e30f;
+    l[i] = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[i][e] = 0.f;
+    tok[i] = row < rows ? row % s.nt : 0;
+    info[i] = tree_row(a, w, s, group, tok[i], tree.anc[tok[i]]);
+  }
+  const float c1 = a.scale * LOG2E;
+  int blk = -1;
+  for (int u = u0; u < u1; ++u) {
+    // keys of the unit: where they lie and how many there are
+    int nk = SAS_BLOCK;
+    const float *kp, *vp;
+    if (u < nu) {
+      blk = u == u0 ? start_s : tree_next(bits, a.words, blk + 1);
+      const size_t at = tree_block_row(a, b, r, blk, &g_tree_attn_err) * D;
+      kp = static_cast<const float*>(a.kc) + at;
+      vp = static_cast<const float*>(a.vc) + at;
+    } else if (u == nu) {
+      nk = s.tail;
+      if (nk == 0) continue;
+      const size_t at = tree_block_row(a, b, r, s.c0, &g_tree_attn_err) * D;
+      kp = static_cast<const float*>(a.kc) + at;
+      vp = static_cast<const float*>(a.vc) + at;
+    } else {
+      nk = s.nt;
+      kp = static_cast<const float*>(a.kd) + group * a.T * D;
+      vp = static_cast<const float*>(a.vd) + group * a.T * D;
+    }
+    __syncthreads();  // the previous unit's tiles are read
+    for (int e = tid; e < SAS_BLOCK * D / 4; e += TA_THREADS) {
+      const int row = e / (D / 4), c = (e % (D / 4)) * 4;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+      if (row < nk) {
+        x = __ldg(reinterpret_cast<const float4*>(kp + (size_t)row * D + c));
+        y = __ldg(reinterpret_cast<const float4*>(vp + (size_t)row * D + c));
+      }
+      *reinterpret_cast<float4*>(ks + row * LD + c) = x;
+      *reinterpret_cast<float4*>(vs + row * D + c) = y;
+    }
+    __syncthreads();
+    float z[TA_WROWS][2];
+#pragma unroll
+    for (int i = 0; i < TA_WROWS; ++i) z[i][0] = z[i][1] = 0.f;
+#pragma unroll 4
+    for (int c = 0; c < D; c += 4) {
+      const float4 k0 = *reinterpret_cast<const float4*>(ks + lane * LD + c);
+      const float4 k1 = *reinterpret_cast<const float4*>(ks + (lane + 32) * LD + c);
+#pragma unroll
+      for (int i = 0; i < TA_WROWS; ++i) {
+        const float4 x = *reinterpret_cast<const float4*>(qs + (wid * TA_WROWS + i) * D + c);
+        z[i][0] = fmaf(x.x, k0.x, fmaf(x.y, k0.y, fmaf(x.z, k0.z, fmaf(x.w, k0.w, z[i][0]))));
+        z[i][1] = fmaf(x.x, k1.x, fmaf(x.y, k1.y, fmaf(x.z, k1.z, fmaf(x.w, k1.w, z[i][1]))));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < TA_WROWS; ++i) {
+      const int row = row0 + wid * TA_WROWS + i;
+      float bias[2] = {-INFINITY, -INFINITY};
+      if (row < rows) {
+        if (u < nu) {
+          const float sc = w.scores[(group * a.T + tok[i]) * (a.N / SAS_BLOCK) + blk];
+          bias[0] = bias[1] = tree_bias(info[i], sc, blk, a.gated) * LOG2E;
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int j = lane + 32 * h;
+            if (u == nu) {
+              if (j < nk) bias[h] = info[i].tail_bias * LOG2E;
+            } else if (j < nk && (tree.anc[tok[i]] >> j & 1ull)) {
+              bias[h] = early_tok >> j & 1ull ? info[i].tail_bias * LOG2E : 0.f;
+            }
+          }
+        }
+      }
+      // a masked key's logit is -inf whatever its product was
+      const float z0 = bias[0] == -INFINITY ? -INFINITY : fmaf(z[i][0], c1, bias[0]);
+      const float z1 = bias[1] == -INFINITY ? -INFINITY : fmaf(z[i][1], c1, bias[1]);
+      const float mx = warp_max(fmaxf(z0, z1));
+      if (!(mx > -INFINITY) && !__any_sync(0xffffffffu, z0 != z0 || z1 != z1)) continue;
+      const float mn = fmaxf(m[i], mx), alpha = exp2f(m[i] - mn);
+      const float p0 = exp2f(z0 - mn), p1 = exp2f(z1 - mn);
+      m[i] = mn;
+      l[i] = l[i] * alpha + warp_sum(p0 + p1);
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[i][e] *= alpha;
+#pragma unroll 4
+      for (int j = 0; j < SAS_BLOCK; ++j) {
+        const float p = __shfl_sync(0xffffffffu, j < 32 ? p0 : p1, j & 31);
+        if (p != 0.f) {  // a masked key's value is not touched
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[i][e] = fmaf(p, vs[j * D + lane * E + e], acc[i][e]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < TA_WROWS; ++i) {
+    const int row = row0 + wid * TA_WROWS + i;
+    if (row >= rows) continue;
+    const size_t at = (group * a.ns + split) * (size_t)(G * a.T) + row;
+    if (lane == 0) w.ml[at] = make_float2(m[i], l[i]);
+    if (l[i] != 0.f) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) w.part[at * D + lane * E + e] = acc[i][e];
+    }
+  }
+}
+
+// Joins the splits: o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s, one
+// warp per row. A split that saw none of a row's keys has l = 0 and wrote no
+// partial output.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) k_tree_join(TreeArgs a, TreeWs w) {
+  constexpr int E = D / 32;
+  const int b = blockIdx.z, r = blockIdx.y, lane = threadIdx.x & 31;
+  const int G = a.Hq / a.Hkv, row = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const TreeSeq s = tree_seq(a, b, nullptr);
+  if (row >= G * s.nt) return;
+  const size_t group = (size_t)b * a.Hkv + r, R = (size_t)G * a.T;
+  const size_t at0 = group * a.ns * R + row;
+  float M = -INFINITY;
+  for (int i = lane; i < a.ns; i += 32) {
+    const float2 ml = w.ml[at0 + i * R];
+    if (ml.y != 0.f) M = fmaxf(M, ml.x);
+  }
+  M = warp_max(M);
+  float L = 0.f, acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  for (int i = 0; i < a.ns; ++i) {
+    const float2 ml = w.ml[at0 + i * R];
+    if (ml.y == 0.f) continue;
+    const float f = exp2f(ml.x - M);
+    L = fmaf(ml.y, f, L);
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      acc[e] = fmaf(w.part[(at0 + i * R) * D + lane * E + e], f, acc[e]);
+  }
+  T* o = static_cast<T*>(a.o) +
+         (((size_t)b * a.Hq + r * G + row / s.nt) * a.T + row % s.nt) * D + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = from_f<T>(acc[e] / L);
+}
+
+// ------------------------------------------------------------------ host
+cudaError_t launch_tree_join(const TreeArgs& a, const TreeWs& w, int bf16, int d,
+                             cudaStream_t st) {
+  const dim3 grid((a.Hq / a.Hkv * a.T + 7) / 8, a.Hkv, a.B);
+  if (bf16) {
+    if (d == 128)
+      k_tree_join<__nv_bfloat16, 128><<<grid, 256, 0, st>>>(a, w);
+    else
+      k_tree_join<__nv_bfloat16, 64><<<grid, 256, 0, st>>>(a, w);
+  } else {
+    if (d == 128)
+      k_tree_join<float, 128><<<grid, 256, 0, st>>>(a, w);
+    else
+      k_tree_join<float, 64><<<grid, 256, 0, st>>>(a, w);
+  }
+  return cudaGetLastError();
+}
+
+template <int D>
+static cudaError_t launch_simt(const TreeArgs& a, const TreeWs& w, cudaStream_t st) {
+  const size_t smem =
+      (size_t)(TA_ROWS * D + SAS_BLOCK * (D + 4) + SAS_BLOCK * D + a.words) * sizeof(float);
+  cudaError_t e = ensure_smem(k_tree_attn_simt<D>, smem);
+  if (e != cudaSuccess) return e;
+  const int rows = a.Hq / a.Hkv * a.T, tiles = (rows + TA_ROWS - 1) / TA_ROWS;
+  k_tree_attn_simt<D><<<dim3(tiles * a.ns, a.Hkv, a.B), TA_THREADS, smem, st>>>(a, w);
+  e = cudaGetLastError();
+  return e != cudaSuccess ? e : launch_tree_join(a, w, 0, D, st);
+}
+
+cudaError_t launch_tree_attn_simt(const TreeArgs& a, const TreeWs& w, int d, cudaStream_t st) {
+  return d == 128 ? launch_simt<128>(a, w, st) : launch_simt<64>(a, w, st);
+}
+
+// Splits of a kv group's units: enough CTAs for two an SM, no more than the
+// units that the tokens can select.
+int tree_splits(int B, int Hq, int Hkv, int T, int N, int topk, int bf16) {
+  const int tile = bf16 ? 128 : TA_ROWS;
+  const long long tiles = ((long long)(Hq / Hkv) * T + tile - 1) / tile;
+  const long long ctas = tiles * Hkv * B;
+  long long units = (long long)T * topk;
+  if (units > N / SAS_BLOCK) units = N / SAS_BLOCK;
+  long long ns = (2 * 148 + ctas / 2) / ctas;
+  if (ns > units + 2) ns = units + 2;
+  if (ns > 32) ns = 32;
+  return ns < 1 ? 1 : (int)ns;
+}
+
+uint32_t* tree_attn_error_word() {
+  void* p = nullptr;
+  cudaGetSymbolAddress(&p, g_tree_attn_err);
+  return static_cast<uint32_t*>(p);
+}
+
+}  // namespace sas

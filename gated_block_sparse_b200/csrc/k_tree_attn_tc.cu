@@ -1,0 +1,488 @@
+// Attention of drafted tokens on the 5th-generation tensor cores (bf16
+// caches): the definition of k_tree_attn.cu, TMA-fed tcgen05 MMAs with TMEM
+// accumulators.
+//
+// One CTA per (128 rows, kv group, split of its units); rows are the group's
+// heads x drafted tokens, so one K/V tile serves them all. Even with few rows
+// the tensor pipe is not the bound: an M = 128 unit (S = Q K^T, O += P V)
+// takes about 740 cycles where an SM's share of HBM needs 1400 for its 32 KB.
+//   warp 4     TMA producers: lane 0 K, lane 1 V of each history unit, each
+//              into its own two-stage ring (a K slot is free once S is done,
+//              a V slot once PV is done);
+//   warp 5     one elected thread issues tcgen05.mma: S_j (M128 N64, two TMEM
+//              buffers) and O += P_j V_j (A = P_j read from TMEM);
+//   warps 0-3  softmax, thread i = row i = TMEM lane i; warps whose rows are
+//              all past the end take no part.
+// The tail and the drafted tokens, which end inside a tile, come first in
+// their split: all threads write them into the ring's stages with zeros
+// behind the last key (whatever the cache holds there, 0 * NaN would reach
+// the sums). A value that is not finite in a block that only some rows keep
+// would reach the others the same way; such a row shows up as a sum that is
+// not finite, and repair_row computes it again key by key.
+// P is rounded to bf16 for its MMA (half a step is 2^-9 of a weight, and the
+// row's sum takes the unrounded weights); everything else is fp32.
+// About 100 KB of shared memory and 256 TMEM columns, so two CTAs an SM.
+#include <cuda.h>
+#include <math.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "ptx.cuh"
+#include "tc.cuh"
+#include "tree.cuh"
+
+namespace sas {
+
+__device__ uint32_t g_tree_tc_err = 0;
+
+namespace {
+
+constexpr int TT_THREADS = 192;
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float RESCALE_LOG2 = 8.0f;  // lazy rescale threshold (log2 units)
+
+template <int D>
+struct Lay {
+  static constexpr uint32_t TILE = 64 * D * 2;    // one K or V block
+  static constexpr uint32_t Q = 0;
+  static constexpr uint32_t KV = Q + 128 * D * 2;  // stage s: K, then V
+  static constexpr uint32_t BAR = KV + 4 * TILE;
+  static constexpr uint32_t BITS = BAR + 128;      // block bitmap
+};
+
+enum Bar {
+  B_KF = 0, B_KE = 2, B_VF = 4, B_VE = 6, B_SF = 8, B_PF = 10, B_OD = 11, NBAR = 12
+};
+static_assert(NBAR * 8 + 4 <= 128, "barriers and the TMEM address fit their 128 bytes");
+
+// O += P V with P (bf16, two per 32-bit column) read from TMEM.
+__device__ __forceinline__ void mma_tmem_a(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Offset of 16-byte piece p of row `row` in a K-major tile of `nrows` rows
+// under the 128-byte swizzle: 64-column chunks one after the other, rows of
+// 128 bytes, the piece's index within the row xor (row mod 8).
+__device__ __forceinline__ uint32_t sw_off(int row, int p, int nrows) {
+  return (uint32_t)((p >> 3) * nrows * 128 + row * 128 + (((p & 7) ^ (row & 7)) << 4));
+}
+
+struct RowState {
+  unsigned long long anc, early;
+  TreeRow info;
+  int tok;
+};
+
+// One row again, key by key, over the units of this split: only keys that the
+// row sees are read, so what other rows' blocks hold does not matter.
+template <int D>
+__device__ __noinline__ float2 repair_row(const TreeArgs& a, const TreeWs& w, const TreeSeq& s,
+                                          const RowState& rs, const uint32_t* bits, int b, int r,
+                                          const __nv_bfloat16* q, int nu, int u0, int u1,
+                                          int start, float* out) {
+  const __nv_bfloat16* kc = static_cast<const __nv_bfloat16*>(a.kc);
+  const __nv_bfloat16* vc = static_cast<const __nv_bfloat16*>(a.vc);
+  const size_t group = (size_t)b * a.Hkv + r;
+  float m = -1e30f, l = 0.f;
+  for (int c = 0; c < D; ++c) out[c] = 0.f;
+  for (int pass = 0; pass < 2; ++pass) {  // the maximum first, then the sums
+    int blk = -1;
+    for (int u = u0; u < u1; ++u) {
+      const __nv_bfloat16 *kp, *vp;
+      int nk = SAS_BLOCK;
+      float bias = rs.info.tail_bias;
+      if (u <= nu) {
+        if (u < nu) {
+          blk = u == u0 ? start : tree_next(bits, a.words, blk + 1);
+          bias = tree_bias(rs.info, w.scores[(group * a.T + rs.tok) * (a.N / SAS_BLOCK) + blk],
+                           blk, a.gated);
+        } else {
+          nk = s.tail;
+        }
+        if (nk == 0 || bias == -INFINITY) continue;
+        const size_t row = tree_block_row(a, b, r, u < nu ? blk : s.c0, nullptr);
+        kp = kc + row * D;
+        vp = vc + row * D;
+      } else {
+        nk = s.nt;
+        kp = static_cast<const __nv_bfloat16*>(a.kd) + group * a.T * D;
+        vp = static_cast<const __nv_bfloat16*>(a.vd) + group * a.T * D;
+      }
+      for (int j = 0; j < nk; ++j) {
+        float bj = bias;
+        if (u > nu) {
+          if (!(rs.anc >> j & 1ull)) continue;
+          if (!(rs.early >> j & 1ull)) bj = 0.f;
+          if (bj == -INFINITY) continue;
+        }
+        float z = 0.f;
+        for (int c = 0; c < D; ++c) z = fmaf(to_f(q[c]), to_f(kp[(size_t)j * D + c]), z);
+        z = (z * a.scale + bj) * LOG2E;
+        if (pass == 0) {
+          m = fmaxf(m, z);
+        } else {
+          const float p = exp2f(z - m);
+          l += p;
+          if (p != 0.f)
+            for (int c = 0; c < D; ++c) out[c] = fmaf(p, to_f(vp[(size_t)j * D + c]), out[c]);
+        }
+      }
+    }
+  }
+  return make_float2(m, l);
+}
+
+}  // namespace
+
+template <int D>
+__global__ void __launch_bounds__(TT_THREADS, 2)
+    k_tree_attn_tc(const __grid_constant__ CUtensorMap kmap,
+                   const __grid_constant__ CUtensorMap vmap, TreeArgs a, TreeWs w) {
+  using L = Lay<D>;
+  constexpr int PC = D / 8;  // 16-byte pieces of a row
+  extern __shared__ __align__(1024) unsigned char sm[];
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::BAR);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::BAR + NBAR * 8);
+  uint32_t* bits = reinterpret_cast<uint32_t*>(sm + L::BITS);
+  __shared__ TreeShared tree;
+  __shared__ int warp_s[TT_THREADS / 32];
+  __shared__ int start_s;
+  uint32_t* err = &g_tree_tc_err;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int r = blockIdx.y, b = blockIdx.z;
+  const int split = blockIdx.x % a.ns, tile = blockIdx.x / a.ns;
+  const int G = a.Hq / a.Hkv;
+  const size_t group = (size_t)b * a.Hkv + r;
+  const TreeSeq s = tree_seq(a, b, nullptr);
+  const int rows = G * s.nt, row0 = tile * 128;
+  if (row0 >= rows) return;
+  if ((smem_u32(sm) & 1023u) != 0) {  // swizzled tiles need 1024-byte alignment
+    if (tid == 0) atomicOr(err, kErrBadIndex);
+    return;
+  }
+  tree_masks(a, b, s.nt, tree, nullptr);
+  int u0, u1;
+  const int nu = tree_units<TT_THREADS>(a, w.ubits + group * a.words, bits, warp_s, &start_s,
+                                        split, u0, u1);
+  // this split's units: the tail and the drafted tokens first, then history
+  const bool has_tail = u0 <= nu && nu < u1 && s.tail > 0;
+  const bool has_draft = u0 <= nu + 1 && nu + 1 < u1;
+  const int nsp = (int)has_tail + (int)has_draft;
+  const int nh = max(0, min(u1, nu) - u0), nunits = nsp + nh;
+  const size_t prow = (group * a.ns + split) * (size_t)(G * a.T) + row0 + tid;
+  if (nunits == 0) {
+    if (tid < 128 && row0 + tid < rows) w.ml[prow] = make_float2(-1e30f, 0.f);
+    return;
+  }
+  const int nwarp = min(4, (rows - row0 + 31) / 32);  // softmax warps with rows
+  if (tid == 0) {
+    for (int i = 0; i < NBAR; ++i) mbar_init(&bars[i], i == B_PF ? nwarp : 1);
+    fence_mbar_init();
+  }
+  if (warp == 5) tc::tmem_alloc(tmem_slot, 256);
+  // Q: rows of the group's heads, zeros behind the last
+  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
+  for (int e = tid; e < 128 * PC; e += TT_THREADS) {
+    const int row = e / PC, p = e % PC, gr = row0 + row;
+    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+    if (gr < rows)
+      x = __ldg(reinterpret_cast<const uint4*>(
+          q + (((size_t)b * a.Hq + r * G + gr / s.nt) * a.T + gr % s.nt) * D + p * 8));
+    *reinterpret_cast<uint4*>(sm + L::Q + sw_off(row, p, 128)) = x;
+  }
+  // the units that end inside a tile
+  for (int j = 0; j < nsp; ++j) {
+    const bool is_tail = has_tail && j == 0;
+    const int nk = is_tail ? s.tail : s.nt;
+    const __nv_bfloat16 *kp, *vp;
+    if (is_tail) {
+      const size_t at = tree_block_row(a, b, r, s.c0, err) * D;
+      kp = static_cast<const __nv_bfloat16*>(a.kc) + at;
+      vp = static_cast<const __nv_bfloat16*>(a.vc) + at;
+    } else {
+      kp = static_cast<const __nv_bfloat16*>(a.kd) + group * a.T * D;
+      vp = static_cast<const __nv_bfloat16*>(a.vd) + group * a.T * D;
+    }
+    unsigned char* st = sm + L::KV + j * 2 * L::TILE;
+    for (int e = tid; e < 64 * PC; e += TT_THREADS) {
+      const int row = e / PC, p = e % PC;
+      uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
+      if (row < nk) {
+        x = __ldg(reinterpret_cast<const uint4*>(kp + (size_t)row * D + p * 8));
+        y = __ldg(reinterpret_cast<const uint4*>(vp + (size_t)row * D + p * 8));
+      }
+      *reinterpret_cast<uint4*>(st + sw_off(row, p, 64)) = x;
+      *reinterpret_cast<uint4*>(st + L::TILE + sw_off(row, p, 64)) = y;
+    }
+  }
+  fence_proxy_async_smem();  // the tiles above are read by the tensor cores
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t tm_s[2] = {tmem, tmem + 64};
+  const uint32_t tm_o = tmem + 128;
+  const int start = nh > 0 ? start_s : 0;
+
+  if (warp == 4) {
+    // ---------------------------------------------------------------- producer
+    if (lane < 2) {
+      const bool kl = lane == 0;
+      const CUtensorMap* map = kl ? &kmap : &vmap;
+      tc::prefetch_map(map);
+      uint64_t* fullb = &bars[kl ? B_KF : B_VF];
+      uint64_t* emptyb = &bars[kl ? B_KE : B_VE];
+      int blk = start - 1;
+      for (int j = 0; j < nunits; ++j) {
+        const int st = j & 1;
+        if (j < nsp) {
+          mbar_arrive(&fullb[st]);  // written above
+          continue;
+        }
+        if (j >= 2) mbar_wait_data(&emptyb[st], ((j >> 1) - 1) & 1, err);
+        blk = tree_next(bits, a.words, blk + 1);
+        int y = 64 * blk, z = (int)group;
+        if (a.table) {
+          z = tree_page(a, b, blk, err) * a.Hkv + r;
+          y = 0;
+        }
+        unsigned char* dst = sm + L::KV + st * 2 * L::TILE + (kl ? 0u : L::TILE);
+        mbar_arrive_expect_tx(&fullb[st], L::TILE);
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+          tc::tma_load_3d(dst + c * 8192, map, 64 * c, y, z, &fullb[st]);
+      }
+    }
+  } else if (warp == 5) {
+    // ---------------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t ID_QK = tc::idesc_bf16(128, 64, 0, 0);
+      constexpr uint32_t ID_PV = tc::idesc_bf16(128, D, 0, 1);
+      const uint32_t q_addr = smem_u32(sm + L::Q);
+      auto pv = [&](int j) {  // O += P_j V_j
+        mbar_wait(&bars[B_PF], j & 1, err);
+        mbar_wait_data(&bars[B_VF + (j & 1)], (j >> 1) & 1, err);
+        tc::fence_after_sync();
+        const uint32_t v_addr = smem_u32(sm + L::KV + (j & 1) * 2 * L::TILE + L::TILE);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {  // P_j: columns 8 ks .. 8 ks + 7 of S_j's buffer
+          const uint64_t bd = tc::sw128_desc(v_addr + ks * 2048, 8192, 1024);
+          mma_tmem_a(tm_o, tm_s[j & 1] + 8 * ks, bd, ID_PV, (j > 0 || ks > 0) ? 1u : 0u);
+        }
+        tc::commit(&bars[B_OD]);
+        tc::commit(&bars[B_VE + (j & 1)]);
+      };
+      for (int j = 0; j < nunits; ++j) {
+        const int st = j & 1;
+        mbar_wait_data(&bars[B_KF + st], (j >> 1) & 1, err);
+        // S_j overwrites P_{j-2} (S_{j-2}'s buffer): PV_{j-2} must have read it
+        if (j >= 2) mbar_wait(&bars[B_OD], (j - 2) & 1, err);
+        tc::fence_after_sync();
+        const uint32_t k_addr = smem_u32(sm + L::KV + st * 2 * L::TILE);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {  // K = D in steps of 16 (32 bytes)
+          const uint32_t c = ks >> 2, off = (ks & 3) * 32;
+          const uint64_t ad = tc::sw128_desc(q_addr + c * 16384 + off, 16, 1024);
+          const uint64_t bd = tc::sw128_desc(k_addr + c * 8192 + off, 16, 1024);
+          tc::mma_bf16(tm_s[st], ad, bd, ID_QK, ks > 0 ? 1u : 0u);
+        }
+        tc::commit(&bars[B_SF + st]);
+        tc::commit(&bars[B_KE + st]);
+        if (j >= 1) pv(j - 1);
+      }
+      pv(nunits - 1);
+    }
+  } else if (warp < nwarp) {
+    // ---------------------------------------------------------------- softmax
+    const int row = row0 + tid;
+    const bool valid = row < rows;
+    const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
+    const float c1 = a.scale * LOG2E, inv_scale = 1.0f / a.scale;
+    RowState rs;
+    rs.tok = valid ? row % s.nt : 0;
+    rs.anc = tree.anc[rs.tok];
+    rs.early = tree_early(tree, s);
+    rs.info = tree_row(a, w, s, group, rs.tok, rs.anc);
+    const float* sc = w.scores + (group * a.T + rs.tok) * (size_t)(a.N / SAS_BLOCK);
+    float m = -1e30f, l = 0.f;
+    int blk = start - 1;
+    float next_score = 0.f;
+    if (nh > 0) {  // the score of the next history unit is loaded a unit ahead
+      blk = start;
+      next_score = sc[blk];
+    }
+    for (int j = 0; j < nunits; ++j) {
+      const int st = j & 1;
+      float bias = 0.f;
+      unsigned long long see = ~0ull;
+      const bool special = j < nsp;
+      const bool is_tail = has_tail && j == 0;
+      if (special) {
+        see = is_tail ? (1ull << s.tail) - 1ull : rs.anc;
+        if (rs.info.tail_bias == -INFINITY) see &= is_tail ? 0ull : ~rs.early;
+      } else {
+        bias = tree_bias(rs.info, next_score, blk, a.gated) * LOG2E;
+        if (j + 1 < nunits) {
+          blk = tree_next(bits, a.words, blk + 1);
+          next_score = sc[blk];
+        }
+      }
+      if (!valid) see = 0ull;
+      const bool dead = bias == -INFINITY || see == 0ull;  // the row sees none of the unit
+      mbar_wait_data(&bars[B_SF + st], (j >> 1) & 1, err);
+      tc::fence_after_sync();
+      float z[64];
+      {
+        float x[32], y[32];
+        tc::tmem_ld32(tm_s[st] + lane_off, x);
+        tc::tmem_ld32(tm_s[st] + lane_off + 32, y);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          z[i] = x[i];
+          z[32 + i] = y[i];
+        }
+      }
+      if (special) {
+        // masked keys to -inf; keys that the path moved into the tail's block
+        // get its gate, in units of the raw products
+        const float g = rs.info.tail_bias == -INFINITY ? 0.f : rs.info.tail_bias * inv_scale;
+        const unsigned long long gate = is_tail ? ~0ull : rs.early;
+#pragma unroll
+        for (int i = 0; i < 64; ++i) {
+          if (gate >> i & 1ull) z[i] += g;
+          if (!(see >> i & 1ull)) z[i] = -INFINITY;
+        }
+      }
+      float zm[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) zm[c] = z[c];
+#pragma unroll
+      for (int i = 4; i < 64; i += 4) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) zm[c] = fmaxf(zm[c], z[i + c]);
+      }
+      // c1 > 0, so the maximum of z c1 + bias is that of z
+      const float mx =
+          dead ? -INFINITY : fmaxf(fmaxf(zm[0], zm[1]), fmaxf(zm[2], zm[3])) * c1 + bias;
+      const float mnew = fmaxf(m, mx);
+      const bool grow = (j == 0) || (mnew > m + RESCALE_LOG2);
+      const float muse = grow ? mnew : m;
+      const float off = bias - muse;
+      float rsum = 0.f;
+      uint32_t pk[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        float p0 = tc::ex2(fmaf(z[2 * i], c1, off)), p1 = tc::ex2(fmaf(z[2 * i + 1], c1, off));
+        p0 = dead ? 0.f : p0;
+        p1 = dead ? 0.f : p1;
+        rsum += p0 + p1;
+        __nv_bfloat162 h2 = __floats2bfloat162_rn(p0, p1);
+        pk[i] = *reinterpret_cast<uint32_t*>(&h2);
+      }
+      if (j > 0) {
+        // PV_{j-1} done before O is rescaled. Waiting on every unit also keeps
+        // this thread within one phase of the O-done barrier.
+        mbar_wait_data(&bars[B_OD], (j - 1) & 1, err);
+        tc::fence_after_sync();
+        const float alpha = grow ? tc::ex2(m - muse) : 1.f;
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            float ov[32];
+            tc::tmem_ld32(tm_o + lane_off + 32 * c, ov);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) ov[i] *= alpha;
+            tc::tmem_st32(tm_o + lane_off + 32 * c, ov);
+          }
+          tc::tmem_wait_st();
+        }
+        l = l * alpha + rsum;
+      } else {
+        l = rsum;
+      }
+      m = muse;
+      // P_j (64 bf16, two per column) over the first half of S_j's buffer
+      {
+        float pf[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) pf[i] = __uint_as_float(pk[i]);
+        tc::tmem_st32(tm_s[st] + lane_off, pf);
+      }
+      tc::tmem_wait_st();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[B_PF]);
+    }
+    // epilogue: the split's sums, and O before the division
+    mbar_wait_data(&bars[B_OD], (nunits - 1) & 1, err);
+    tc::fence_after_sync();
+    float* out = w.part + prow * D;
+    bool bad = !(fabsf(l) < INFINITY);
+#pragma unroll 1
+    for (int c = 0; c < D / 32; ++c) {
+      float ov[32];
+      tc::tmem_ld32(tm_o + lane_off + 32 * c, ov);
+      tc::tmem_wait_ld();
+      if (valid) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) bad |= !(fabsf(ov[i]) < INFINITY);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<float4*>(out + 32 * c + 4 * i) =
+              make_float4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
+      }
+    }
+    if (valid) {
+      float2 ml = make_float2(m, l);
+      if (bad)
+        ml = repair_row<D>(a, w, s, rs, bits, b, r,
+                           q + (((size_t)b * a.Hq + r * G + row / s.nt) * a.T + rs.tok) * D, nu,
+                           u0, u1, start, out);
+      w.ml[prow] = ml;
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 5) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 256);
+  }
+}
+
+// ------------------------------------------------------------------ host
+template <int D>
+static cudaError_t launch_tc(const TreeArgs& a, const TreeWs& w, cudaStream_t st) {
+  CUtensorMap km, vm;
+  const int rpp = a.table ? SAS_BLOCK : a.N, planes = (a.table ? a.npages : a.B) * a.Hkv;
+  if (!make_tma_map_bf16_3d(&km, a.kc, D, rpp, planes) ||
+      !make_tma_map_bf16_3d(&vm, a.vc, D, rpp, planes))
+    return cudaErrorInvalidValue;
+  const size_t smem = Lay<D>::BITS + (size_t)a.words * sizeof(uint32_t);
+  cudaError_t e = ensure_smem(k_tree_attn_tc<D>, smem);
+  if (e != cudaSuccess) return e;
+  const int rows = a.Hq / a.Hkv * a.T, tiles = (rows + 127) / 128;
+  k_tree_attn_tc<D><<<dim3(tiles * a.ns, a.Hkv, a.B), TT_THREADS, smem, st>>>(km, vm, a, w);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_tree_join(a, w, 1, D, st);
+}
+
+cudaError_t launch_tree_attn_tc(const TreeArgs& a, const TreeWs& w, int d, cudaStream_t st) {
+  return d == 128 ? launch_tc<128>(a, w, st) : launch_tc<64>(a, w, st);
+}
+
+uint32_t* tree_tc_error_word() {
+  void* p = nullptr;
+  cudaGetSymbolAddress(&p, g_tree_tc_err);
+  return static_cast<uint32_t*>(p);
+}
+
+}  // namespace sas

@@ -169,6 +169,58 @@ cudaError_t launch_attn_bwd_tc_tokens(const void* q, const void* k, const void* 
                                       void* ws, cudaStream_t st);
 uint32_t* attn_bwd_tc_error_word();
 
+// ---- serving (sas_serving.h)
+// A tensor of H heads to rotate: element strides of (batch, head, token).
+struct RotaryTensor {
+  const void* x;
+  void* y;
+  int H;
+  long long xs[3], ys[3];
+};
+cudaError_t launch_rotary(const RotaryTensor& q, const RotaryTensor& k, int bf16, int B, int N,
+                          int d, const float* inv_freq, int rot, int interleaved, float amp,
+                          int inverse, const int32_t* pos, const int32_t* start,
+                          const int32_t* parents, cudaStream_t st);
+uint32_t* rotary_error_word();
+
+struct PageMapArgs {
+  const int32_t *lens, *nnew;
+  int32_t* table;
+  const int32_t *free_pages, *free_head;
+  int32_t *slots, *new_lens, *taken, *head_out;
+  int B, T, width, npages, nfree;
+};
+cudaError_t launch_page_map(const PageMapArgs& a, cudaStream_t st);
+uint32_t* pages_error_word();
+
+struct AppendArgs {
+  const void *q, *k, *v;
+  void *qo, *kc, *vc, *ksum;
+  long long qs[3], ks[3], vs[3];  // element strides of (batch, head, token)
+  const int32_t *rows, *lens, *ntok, *slots;
+  const float* inv_freq;
+  float amp;
+  int B, Hq, Hkv, T, N, npages, rot, interleaved, sum_bf16, hslice;
+};
+cudaError_t launch_append(const AppendArgs& a, int bf16, int d, cudaStream_t st);
+uint32_t* append_error_word();
+
+struct TreeArgs {
+  const void *q, *kd, *vd, *kc, *vc, *ksum;
+  const int32_t *parents, *ntok, *lens, *table;
+  void* o;
+  int32_t* idx_out;
+  float scale;
+  int B, Hq, Hkv, T, N, npages, topk, gated;
+  int words, ns;  // 32-block words of a group's bitmap; splits of its units
+};
+int tree_splits(int B, int Hq, int Hkv, int T, int N, int topk, int bf16);
+size_t tree_ws_bytes(int B, int Hq, int Hkv, int T, int N, int d, int topk, int bf16);
+cudaError_t launch_tree(TreeArgs a, int bf16, int sum_bf16, int d, void* ws, cudaStream_t st);
+uint32_t* tree_select_error_word();
+uint32_t* tree_attn_error_word();
+uint32_t* tree_tc_error_word();
+
 // Self-test of the bounded wait (k_status.cu): one warp waits on a barrier
 // that nothing completes; after the wait limit it records kErrWaitTimeout in
 // its own error word.

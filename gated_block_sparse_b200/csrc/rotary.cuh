@@ -1,0 +1,113 @@
+// Rotary positions: the angle of a (position, pair) and the rotation of the
+// pairs that one thread holds. Shared by the rotation alone (k_rotary.cu) and
+// the cache write (k_append.cu).
+//
+// Pair p of a head has the frequency f_p (fp32, radians per position) and is
+// turned by theta = pos f_p:
+//   y0 = A (x0 cos theta - x1 sin theta), y1 = A (x1 cos theta + x0 sin theta),
+// elements (p, p + rot/2) of the head in the half layout, (2p, 2p + 1) in the
+// interleaved one. The transpose (the backward pass) turns by -theta.
+//
+// theta reaches 5e5 radians at the end of a 512K context, where an fp32
+// product is off by up to 0.03 radians. So the frequency is kept in turns as a
+// 64-bit binary fraction, F = frac(f / 2 pi) 2^64: pos * F modulo 2^64 is the
+// fraction of the last turn, wrapping exactly, and the error is that of F,
+// 2^-53 f / 2 pi turns a position (2e-11 turns at 2^20 positions and f = 1).
+// The top 32 bits give the nearest quarter turn and an offset of at most an
+// eighth, whose fp32 rounding is below 3e-8 of a turn's eighth.
+#pragma once
+
+#include "common.cuh"
+
+namespace sas {
+
+__device__ __forceinline__ unsigned long long turns_u64(float f) {
+  const double t = (double)f * 0.15915494309189533577;  // 1 / (2 pi)
+  return __double2ull_rd((t - floor(t)) * 18446744073709551616.0);
+}
+
+__device__ __forceinline__ void turn_sincos(unsigned long long F, int pos, float amp, float& c,
+                                            float& s) {
+  const unsigned long long ph = F * (unsigned long long)(long long)pos;
+  const uint32_t t = (uint32_t)(ph >> 32);
+  const uint32_t quarter = (t + 0x20000000u) >> 30;  // nearest quarter turn (mod 4)
+  const int off = (int)(t - (quarter << 30));        // [-2^29, 2^29): an eighth of a turn
+  float sn, cs;
+  sincospif((float)off * 4.656612873077393e-10f, &sn, &cs);  // off 2^-31 half turns
+  const float a = (quarter & 1u) ? sn : cs, b = (quarter & 1u) ? cs : sn;
+  c = ((quarter == 1u || quarter == 2u) ? -a : a) * amp;
+  s = ((quarter & 2u) ? -b : b) * amp;
+}
+
+// 2 VN elements of a head: VN pairs. VN = Vec16<T>::N moves 16-byte vectors,
+// VN = 1 single elements (rotated widths or strides that vectors do not fit).
+// p0 and p1 are where the two halves start: VN elements from each (half
+// layout, or an unrotated stretch), or 2 VN elements from p0 (interleaved,
+// p1 = p0 + VN).
+template <typename T, int VN>
+__device__ __forceinline__ void load_vec(const T* p, float (&x)[VN]) {
+  if constexpr (VN == 1)
+    x[0] = to_f(*p);
+  else
+    Vec16<T>::load(p, x);
+}
+template <typename T, int VN>
+__device__ __forceinline__ void store_vec(T* p, const float (&x)[VN]) {
+  if constexpr (VN == 1)
+    *p = from_f<T>(x[0]);
+  else
+    Vec16<T>::store(p, x);
+}
+
+// Where unit u (2 VN elements) of a head lies: its two element offsets.
+// Units u < rot / (2 VN) are rotated, the others are passed through.
+template <int VN>
+__device__ __forceinline__ void unit_offsets(int u, int rot, bool interleaved, int& e0, int& e1) {
+  const int ru = rot / (2 * VN);
+  if (u < ru && !interleaved) {
+    e0 = u * VN;
+    e1 = (rot >> 1) + u * VN;
+  } else {
+    e0 = 2 * u * VN;
+    e1 = e0 + VN;
+  }
+}
+
+// Rotates the VN pairs of (a, b): element i of a with element i of b (half
+// layout), or neighbours within a, then within b (interleaved).
+template <int VN>
+__device__ __forceinline__ void rotate_unit(float (&a)[VN], float (&b)[VN], const float (&c)[VN],
+                                            const float (&s)[VN], bool interleaved) {
+  if (VN > 1 && interleaved) {
+#pragma unroll
+    for (int i = 0; i < VN / 2; ++i) {
+      const float a0 = a[2 * i], a1 = a[2 * i + 1], b0 = b[2 * i], b1 = b[2 * i + 1];
+      a[2 * i] = a0 * c[i] - a1 * s[i];
+      a[2 * i + 1] = a1 * c[i] + a0 * s[i];
+      b[2 * i] = b0 * c[VN / 2 + i] - b1 * s[VN / 2 + i];
+      b[2 * i + 1] = b1 * c[VN / 2 + i] + b0 * s[VN / 2 + i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VN; ++i) {
+      const float x0 = a[i], x1 = b[i];
+      a[i] = x0 * c[i] - x1 * s[i];
+      b[i] = x1 * c[i] + x0 * s[i];
+    }
+  }
+}
+
+// cos and sin of the VN pairs of rotated unit u at a position: pairs u VN ..
+// u VN + VN - 1 in both layouts.
+template <int VN>
+__device__ __forceinline__ void unit_sincos(const float* __restrict__ inv_freq, int u, int pos,
+                                            float amp, bool inverse, float (&c)[VN],
+                                            float (&s)[VN]) {
+#pragma unroll
+  for (int i = 0; i < VN; ++i) {
+    turn_sincos(turns_u64(__ldg(inv_freq + u * VN + i)), pos, amp, c[i], s[i]);
+    if (inverse) s[i] = -s[i];
+  }
+}
+
+}  // namespace sas

@@ -1,0 +1,241 @@
+// A tree of drafted tokens beside a cache: what its kernels share.
+//
+// Sequence b has lens[b] = n cached tokens and up to T <= 64 drafted ones with
+// a parent each (-1: the last cached token). Token i sits at position
+// n + depth_i and sees the cache and its ancestors, itself included, exactly
+// as if the path from the root to it had been appended to the cache:
+//   C_i = (n + depth_i) / 64 history blocks, c0 = n / 64 of them whole in the
+//   cache. A path that fills the block of the cache's tail (its
+//   n - 64 c0 < 64 last tokens) makes it history block c0 of that token, with
+//   a summary of its own: the mean of the tail's keys and of the path's keys
+//   up to it. A path has at most 64 tokens, so it fills at most that one.
+#pragma once
+
+#include <math.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace sas {
+
+constexpr int TREE_MAX = 64;  // drafted tokens of a sequence: one 64-bit mask a token
+
+// The tree of one sequence, in shared memory.
+struct TreeShared {
+  unsigned long long anc[TREE_MAX];  // ancestors of token i, i included
+  int up[TREE_MAX];
+};
+
+struct TreeSeq {
+  int n;      // cached tokens
+  int nt;     // drafted tokens
+  int c0;     // whole blocks of the cache
+  int tail;   // cached tokens past them
+};
+
+// Lengths of sequence b, clamped to the buffers (a length outside them is
+// reported by the caller that passes err).
+__device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b, uint32_t* err) {
+  TreeSeq s;
+  const int n = a.lens[b], nt = a.ntok ? a.ntok[b] : a.T;
+  s.n = min(max(n, 0), a.N);
+  s.nt = min(max(nt, 0), a.T);
+  if (err && (s.n != n || s.nt != nt)) atomicOr(err, kErrBadIndex);
+  s.c0 = s.n / SAS_BLOCK;
+  s.tail = s.n - s.c0 * SAS_BLOCK;
+  return s;
+}
+
+// Ancestor masks by pointer jumping: after round e a token's mask holds its
+// 2^(e+1) nearest ancestors. A parent that is not below its child is reported
+// and read as -1. All threads of the block (at least TREE_MAX) call it; it
+// ends with a barrier. No parents: a chain.
+__device__ __forceinline__ void tree_masks(const TreeArgs& a, int b, int nt, TreeShared& t,
+                                           uint32_t* err) {
+  const int i = threadIdx.x;
+  if (!a.parents) {
+    if (i < TREE_MAX) t.anc[i] = ~0ull >> (63 - i);
+    __syncthreads();
+    return;
+  }
+  if (i < TREE_MAX) {
+    int p = -1;
+    if (i < nt) {
+      p = a.parents[(size_t)b * a.T + i];
+      if (p < -1 || p >= i) {
+        if (err) atomicOr(err, kErrBadIndex);
+        p = -1;
+      }
+    }
+    t.anc[i] = 1ull << i;
+    t.up[i] = p;
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int e = 0; e < 6; ++e) {
+    unsigned long long m = 0;
+    int p = -1;
+    if (i < TREE_MAX) {
+      m = t.anc[i];
+      p = t.up[i];
+      if (p >= 0) {
+        m |= t.anc[p];
+        p = t.up[p];
+      }
+    }
+    __syncthreads();
+    if (i < TREE_MAX) {
+      t.anc[i] = m;
+      t.up[i] = p;
+    }
+    __syncthreads();
+  }
+}
+
+__device__ __forceinline__ int tree_depth(unsigned long long anc) { return __popcll(anc) - 1; }
+
+// Page of logical block m of sequence b (an id outside the pool is reported
+// and replaced by page 0, as in the paged decode).
+__device__ __forceinline__ int tree_page(const TreeArgs& a, int b, int m, uint32_t* err) {
+  const int p = a.table[(size_t)b * (a.N / SAS_BLOCK) + m];
+  if (p >= 0 && p < a.npages) return p;
+  if (err) atomicOr(err, kErrBadIndex);
+  return 0;
+}
+
+// First row of logical block m of head r, in rows of the cache.
+__device__ __forceinline__ size_t tree_block_row(const TreeArgs& a, int b, int r, int m,
+                                                 uint32_t* err) {
+  if (a.table) return ((size_t)tree_page(a, b, m, err) * a.Hkv + r) * SAS_BLOCK;
+  return ((size_t)b * a.Hkv + r) * a.N + (size_t)m * SAS_BLOCK;
+}
+
+// order-preserving map of a score to an unsigned integer (-0 becomes +0, so
+// that exact ties are equal keys)
+__device__ __forceinline__ uint32_t score_key(float s) {
+  const uint32_t u = __float_as_uint(s + 0.f);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float score_of(uint32_t key) {
+  return __uint_as_float((key & 0x80000000u) ? (key & 0x7fffffffu) : ~key);
+}
+
+// What selection leaves of a row (sequence, kv group, drafted token): with
+// the scores themselves it says which blocks the row keeps and their gates,
+// so no list has to be searched and nothing is written per block.
+struct __align__(16) TreeRow {
+  float lse;        // log sum exp of the row's scores
+  uint32_t th;      // key of the lowest kept score
+  int last;         // the kept blocks of that score are those up to this one
+  float tail_bias;  // log g of block c0 (-inf: not kept; 0: not yet filled)
+};
+
+// Bias of history block m: log g, or -inf when the row does not keep it.
+__device__ __forceinline__ float tree_bias(const TreeRow& t, float score, int m, int gated) {
+  const uint32_t key = score_key(score);
+  const bool keep = key > t.th || (key == t.th && m <= t.last);
+  return keep ? (gated ? score - t.lse : 0.f) : -INFINITY;
+}
+
+// Workspace of one call.
+struct TreeWs {
+  float* scores;    // [row][N / 64]
+  TreeRow* rows;    // [row]
+  uint32_t* ubits;  // [group][words]: blocks that some token selected
+  float* part;      // [group][split][G T][d]: outputs before the division
+  float2* ml;       // [group][split][G T]: running maximum (log2 units) and sum
+};
+
+cudaError_t launch_tree_select(const TreeArgs& a, const TreeWs& w, int bf16, int sum_bf16, int d,
+                               cudaStream_t st);
+cudaError_t launch_tree_attn_simt(const TreeArgs& a, const TreeWs& w, int d, cudaStream_t st);
+cudaError_t launch_tree_attn_tc(const TreeArgs& a, const TreeWs& w, int d, cudaStream_t st);
+cudaError_t launch_tree_join(const TreeArgs& a, const TreeWs& w, int bf16, int d,
+                             cudaStream_t st);
+
+// The row of token i; without selection (topk 0) it keeps no block, and none
+// of the tail's once its path has filled that block.
+__device__ __forceinline__ TreeRow tree_row(const TreeArgs& a, const TreeWs& w, const TreeSeq& s,
+                                            size_t group, int i, unsigned long long anc) {
+  if (a.topk > 0) return w.rows[group * a.T + i];
+  TreeRow t;
+  t.lse = 0.f;
+  t.th = 0xffffffffu;
+  t.last = -1;
+  t.tail_bias = s.tail + tree_depth(anc) >= SAS_BLOCK ? -INFINITY : 0.f;
+  return t;
+}
+
+// Drafted tokens whose key lies inside the tail's block.
+__device__ __forceinline__ unsigned long long tree_early(const TreeShared& t, const TreeSeq& s) {
+  unsigned long long m = 0;
+  for (int j = 0; j < s.nt; ++j)
+    if (s.tail + tree_depth(t.anc[j]) < SAS_BLOCK) m |= 1ull << j;
+  return m;
+}
+
+// The units of one split of a (sequence, kv group): the blocks that some
+// token selected, ascending, then the tail (unit nu) and the drafted tokens
+// (unit nu + 1). A split takes units [u0, u1) of the nu + 2. `bits` gets the
+// group's block bitmap; *start the block of unit u0 (when u0 < nu). All
+// THREADS threads of the block call it; it ends with a barrier.
+template <int THREADS>
+__device__ __forceinline__ int tree_units(const TreeArgs& a, const uint32_t* __restrict__ ubits,
+                                          uint32_t* bits, int* warp_s, int* start, int split,
+                                          int& u0, int& u1) {
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  int nu = 0;
+  if (a.topk > 0) {
+    const int per = (a.words + THREADS - 1) / THREADS;
+    const int lo = min(tid * per, a.words), hi = min(lo + per, a.words);
+    int c = 0;
+    for (int i = lo; i < hi; ++i) {
+      bits[i] = ubits[i];
+      c += __popc(bits[i]);
+    }
+    int v = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += y;
+    }
+    if (lane == 31) warp_s[wid] = v;
+    __syncthreads();
+    int before = v - c;
+#pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i) {
+      before += i < wid ? warp_s[i] : 0;
+      nu += warp_s[i];
+    }
+    u0 = (nu + 2) * split / a.ns;
+    if (before <= u0 && u0 < before + c) {  // unit u0 is among this thread's blocks
+      int left = u0 - before;
+      for (int i = lo; i < hi; ++i) {
+        uint32_t word = bits[i];
+        const int pc = __popc(word);
+        if (left < pc) {
+          for (; left > 0; --left) word &= word - 1;
+          *start = i * 32 + __ffs(word) - 1;
+          break;
+        }
+        left -= pc;
+      }
+    }
+    __syncthreads();
+  }
+  u0 = (nu + 2) * split / a.ns;
+  u1 = (nu + 2) * (split + 1) / a.ns;
+  return nu;
+}
+
+// Smallest selected block >= from; -1 past the end.
+__device__ __forceinline__ int tree_next(const uint32_t* bits, int words, int from) {
+  for (int i = from >> 5; i < words; ++i) {
+    const uint32_t word = bits[i] & (i == (from >> 5) ? ~0u << (from & 31) : ~0u);
+    if (word) return i * 32 + __ffs(word) - 1;
+  }
+  return -1;
+}
+
+}  // namespace sas

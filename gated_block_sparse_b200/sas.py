@@ -1,4 +1,5 @@
-"""Python binding of libsas (include/sas.h): argument marshalling only.
+"""Python binding of libsas (include/sas.h, include/sas_serving.h): argument
+marshalling only.
 
 Each function has the name of the C entry point it calls. Tensors are torch
 CUDA tensors (torch provides device memory and the current stream); every step
@@ -68,6 +69,14 @@ SIGNATURES = {
                             _P]),
     "sas_device_status": (_I, [_I, _P]),
     "sas_debug_wait_timeout": (_I, [_P]),
+    "sas_rotary": (_I, [_P, _P, _P, _P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _I, _I, _F,
+                        _I, _P, _P, _P, _P]),
+    "sas_page_map": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P]),
+    "sas_cache_append": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P,
+                              _I, _I, _F, _P, _P, _P, _I, _I, _P, _I, _P]),
+    "sas_decode_tree_workspace_size": (_Z, [_I, _I, _I, _I, _I, _I, _I, _I]),
+    "sas_decode_tree": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _I,
+                             _P, _I, _I, _I, _F, _P, _P, _P, _Z, _P]),
 }
 
 _lib = None
@@ -463,3 +472,206 @@ def sas_debug_wait_timeout(stream=None) -> None:
     """Launch the self-test kernel whose wait nothing completes (gives up after 200 ms)."""
     lib = load_library()
     _check("sas_debug_wait_timeout", lib.sas_debug_wait_timeout(_stream(stream)))
+
+
+# ---------------------------------------------------------------- serving
+# The calls of include/sas_serving.h check what the C side cannot see: every
+# tensor's device, element type and shape. They run on the tensors' device,
+# whatever the current one is, and take their outputs and workspace from the
+# stream that they launch on.
+
+
+class _On:
+    """Device and stream of one call: `with _On(stream, tensors) as st:`."""
+
+    def __init__(self, stream, *tensors):
+        devs = {t.device for t in tensors if t is not None}
+        if len(devs) != 1 or not next(iter(devs)).type == "cuda":
+            raise ValueError("tensors must all be on one CUDA device")
+        self.device = devs.pop()
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        elif stream.device != self.device:
+            raise ValueError(f"stream is on {stream.device}, the tensors are on {self.device}")
+        self.stream = stream
+        self.ctx = torch.cuda.stream(stream)  # also makes the stream's device current
+
+    def __enter__(self):
+        self.ctx.__enter__()
+        return self.stream.cuda_stream
+
+    def __exit__(self, *exc):
+        return self.ctx.__exit__(*exc)
+
+
+def _arg(t, name: str, dtype, shape) -> int | None:
+    """Pointer of a contiguous tensor of this type and shape (None passes)."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+    return _ptr(t)
+
+
+def _strided(t, name: str, dtype, shape):
+    """Pointer and element strides {batch, head, token} of a tensor whose rows
+    are contiguous."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+    if t.stride(-1) != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    return t.data_ptr(), (ctypes.c_int64 * 3)(*t.stride()[:3])
+
+
+def sas_rotary(q, inv_freq, k=None, pos=None, start=None, parents=None, interleaved: bool = False,
+               amplitude: float = 1.0, inverse: bool = False, out=None, stream=None):
+    """Rotary positions of q [B][Hq][N][d] and k [B][Hkv][N][d]; returns qo, or (qo, ko).
+
+    q and k may be strided views (a fused projection's) with contiguous rows.
+    inv_freq [rot/2] fp32 sets the frequencies and the rotated width; the
+    positions are pos [B][N], or start [B] (0 if None) plus the token's index,
+    or plus its depth in the tree of parents [B][N]. inverse=True is the
+    transpose: it takes the gradients of the outputs to those of the inputs.
+    out: qo, or (qo, ko); q and k themselves rotate in place.
+    """
+    B, Hq, N, d = q.shape
+    Hkv = 0 if k is None else k.shape[1]
+    _dt(q)
+    with _On(stream, q, k, inv_freq, pos, start, parents) as st:
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            if k is not None:
+                out = (out, torch.empty(k.shape, dtype=k.dtype, device=k.device))
+        qo, ko = (out, None) if k is None else out
+        if any(t is not None and t.device != q.device for t in (qo, ko)):
+            raise ValueError("tensors must all be on one CUDA device")
+        pq, sq = _strided(q, "q", q.dtype, (B, Hq, N, d))
+        pqo, sqo = _strided(qo, "qo", q.dtype, (B, Hq, N, d))
+        pk = sk = pko = sko = None
+        if k is not None:
+            pk, sk = _strided(k, "k", q.dtype, (B, Hkv, N, d))
+            pko, sko = _strided(ko, "ko", q.dtype, (B, Hkv, N, d))
+        _check("sas_rotary", load_library().sas_rotary(
+            pq, sq, pqo, sqo, Hq, pk, sk, pko, sko, Hkv, _dt(q), B, N, d,
+            _arg(inv_freq, "inv_freq", torch.float32, (inv_freq.numel(),)), 2 * inv_freq.numel(),
+            int(bool(interleaved)), float(amplitude), int(bool(inverse)),
+            _arg(pos, "pos", torch.int32, (B, N)), _arg(start, "start", torch.int32, (B,)),
+            _arg(parents, "parents", torch.int32, (B, N)), st))
+    return out
+
+
+def sas_page_map(lens, nnew, block_table, free_pages, free_head, T: int, npages: int, out=None,
+                 stream=None):
+    """Pages and slots of nnew [B] <= T new tokens after lens [B] cached ones.
+
+    Takes pages from free_pages[free_head:] into block_table [B][width] (in
+    place) and returns (slots [B][T], new_lens [B], taken [B], head [1]), all
+    int32. out supplies the four; new_lens may be lens and head free_head.
+    """
+    i32 = torch.int32
+    (B,), width, nfree = lens.shape, block_table.shape[1], free_pages.numel()
+    with _On(stream, lens, nnew, block_table, free_pages, free_head, *(out or ())) as st:
+        if out is None:
+            new = dict(dtype=i32, device=lens.device)
+            out = (torch.empty((B, T), **new), torch.empty(B, **new), torch.empty(B, **new),
+                   torch.empty(1, **new))
+        slots, new_lens, taken, head = out
+        _check("sas_page_map", load_library().sas_page_map(
+            _arg(lens, "lens", i32, (B,)), _arg(nnew, "nnew", i32, (B,)),
+            _arg(block_table, "block_table", i32, (B, width)),
+            _arg(free_pages, "free_pages", i32, (nfree,)),
+            _arg(free_head, "free_head", i32, (1,)), B, T, width, npages, nfree,
+            _arg(slots, "slots", i32, (B, T)), _arg(new_lens, "new_lens", i32, (B,)),
+            _arg(taken, "taken", i32, (B,)), _arg(head, "head", i32, (1,)), st))
+    return out
+
+
+def sas_cache_append(k, v, lens, kc, vc, ksum=None, ntok=None, rows=None, slots=None,
+                     inv_freq=None, interleaved: bool = False, amplitude: float = 1.0, q=None,
+                     out=None, stream=None):
+    """Write new tokens' k, v [B][Hkv][T][d] into a cache, in place.
+
+    The cache is kc, vc [B][Hkv][Lmax][d], or with slots [B][T] the pools
+    [npages][Hkv][64][d]; ksum [B][Hkv][Lmax/64][d] or [npages][Hkv][d] (fp32
+    or bf16) gets the summaries of the blocks that become complete. ntok [B]
+    counts the tokens (all T if None), rows [B][T] picks their rows of k and v.
+    With inv_freq, k is rotated at its position first, and q [B][Hq][T][d],
+    when given, beside it: returns qo (out supplies it), else None.
+    """
+    i32 = torch.int32
+    B, Hkv, T, d = k.shape
+    lib, dt = load_library(), _dt(k)
+    with _On(stream, k, v, lens, kc, vc, ksum, ntok, rows, slots, inv_freq, q, out) as st:
+        if slots is None:
+            N, npages = kc.shape[2], 0
+            cshape, sshape = (B, Hkv, N, d), (B, Hkv, N // 64, d)
+        else:
+            N, npages = 0, kc.shape[0]
+            cshape, sshape = (npages, Hkv, 64, d), (npages, Hkv, d)
+        pq = sq = None
+        Hq = Hkv
+        if q is not None:
+            Hq = q.shape[1]
+            pq, sq = _strided(q, "q", k.dtype, (B, Hq, T, d))
+            if out is None:
+                out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        elif out is not None:
+            raise ValueError("out goes with q")
+        pk, sk = _strided(k, "k", k.dtype, (B, Hkv, T, d))
+        pv, sv = _strided(v, "v", k.dtype, (B, Hkv, T, d))
+        nf = 0 if inv_freq is None else inv_freq.numel()
+        _check("sas_cache_append", lib.sas_cache_append(
+            pq, sq, _arg(out, "out", k.dtype, (B, Hq, T, d)), pk, sk, pv, sv, dt, B, Hq, Hkv, T,
+            d, _arg(rows, "rows", i32, (B, T)), _arg(lens, "lens", i32, (B,)),
+            _arg(ntok, "ntok", i32, (B,)), _arg(inv_freq, "inv_freq", torch.float32, (nf,)),
+            2 * nf, int(bool(interleaved)), float(amplitude), _arg(slots, "slots", i32, (B, T)),
+            _arg(kc, "kc", k.dtype, cshape), _arg(vc, "vc", k.dtype, cshape), N, npages,
+            None if ksum is None else _arg(ksum, "ksum", ksum.dtype, sshape),
+            SAS_F32 if ksum is None else _dt(ksum), st))
+    return out
+
+
+def sas_decode_tree(q, kd, vd, kc, vc, lens, ksum, topk: int, parents=None, ntok=None,
+                    block_table=None, gated: int = 1, scale: float = 0.0, out=None, idx_out=None,
+                    ws=None, stream=None):
+    """Decode of a tree of drafted tokens: q [B][Hq][T][d], kd, vd [B][Hkv][T][d]
+    over caches as sas_decode's (or, with block_table, sas_decode_paged's) ->
+    o [B][Hq][T][d].
+
+    parents [B][T]: each token's parent among the drafted ones, below it, or -1
+    (a chain if None). ntok [B] counts the drafted tokens (all T if None); rows
+    from ntok on are left as they were in out and idx_out [B][Hkv][T][topk].
+    """
+    i32 = torch.int32
+    B, Hq, T, d = q.shape
+    Hkv = kd.shape[1]
+    lib, dt = load_library(), _dt(q)
+    with _On(stream, q, kd, vd, kc, vc, lens, ksum, parents, ntok, block_table, out, idx_out,
+             ws) as st:
+        if block_table is None:
+            N, npages = kc.shape[2], 0
+            cshape, sshape = (B, Hkv, N, d), (B, Hkv, N // 64, d)
+        else:
+            N, npages = 64 * block_table.shape[1], kc.shape[0]
+            cshape, sshape = (npages, Hkv, 64, d), (npages, Hkv, d)
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        need = lib.sas_decode_tree_workspace_size(B, Hq, Hkv, T, N, d, topk, dt)
+        w = _ws(need, q.device, ws)
+        _check("sas_decode_tree", lib.sas_decode_tree(
+            _arg(q, "q", q.dtype, (B, Hq, T, d)), _arg(kd, "kd", q.dtype, (B, Hkv, T, d)),
+            _arg(vd, "vd", q.dtype, (B, Hkv, T, d)), _arg(kc, "kc", q.dtype, cshape),
+            _arg(vc, "vc", q.dtype, cshape), dt, B, Hq, Hkv, T, N, d,
+            _arg(parents, "parents", i32, (B, T)), _arg(ntok, "ntok", i32, (B,)),
+            _arg(lens, "lens", i32, (B,)),
+            None if ksum is None else _arg(ksum, "ksum", ksum.dtype, sshape),
+            SAS_F32 if ksum is None else _dt(ksum),
+            _arg(block_table, "block_table", i32, (B, N // 64)), npages, topk, int(gated),
+            float(scale), _arg(out, "out", q.dtype, (B, Hq, T, d)),
+            _arg(idx_out, "idx_out", i32, (B, Hkv, T, topk)) if topk else None, _ptr(w),
+            w.numel() * w.element_size(), st))
+    return out
