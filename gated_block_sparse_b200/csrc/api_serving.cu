@@ -18,8 +18,9 @@ void set_strides(long long (&out)[3], const int64_t* in, int H, int N, int d) {
   out[2] = in ? in[2] : d;
 }
 
-// Dimensions of one element never use their stride.
+// Dimensions of one element never use their stride, and no heads use none.
 bool strides_ok(const long long (&s)[3], int B, int H, int N, long long least) {
+  if (H == 0) return true;
   return (B <= 1 || s[0] >= least) && (H <= 1 || s[1] >= least) && (N <= 1 || s[2] >= least);
 }
 

@@ -9,6 +9,7 @@ fallback: if libsas.so is missing or no GPU is present, calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -476,59 +477,79 @@ def sas_debug_wait_timeout(stream=None) -> None:
 
 # ---------------------------------------------------------------- serving
 # The calls of include/sas_serving.h check what the C side cannot see: every
-# tensor's device, element type and shape. They run on the tensors' device,
-# whatever the current one is, and take their outputs and workspace from the
-# stream that they launch on.
+# tensor's device, element type and shape. They run on the device of their
+# first tensor, whatever the current one is, and take outputs and workspace
+# from the stream that they launch on. Small steps are bound by this host
+# code, so it makes each check once and opens a stream or device context only
+# where the current one is another.
 
 
-class _On:
-    """Device and stream of one call: `with _On(stream, tensors) as st:`."""
+# Handle of a device's current stream, without the Stream object around it
+# (0.1 us against 3 us of torch.cuda.current_stream).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
-    def __init__(self, stream, *tensors):
-        devs = {t.device for t in tensors if t is not None}
-        if len(devs) != 1 or not next(iter(devs)).type == "cuda":
+
+def _like(t):
+    """An uninitialised contiguous tensor of t's shape, type and device."""
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
+
+
+def _placed(fn):
+    """Run fn on its first tensor's device and, when given, on `stream`."""
+    @functools.wraps(fn)
+    def call(t, *args, stream=None, **kw):
+        dev = t.get_device()
+        if dev < 0:
             raise ValueError("tensors must all be on one CUDA device")
-        self.device = devs.pop()
-        if stream is None:
-            stream = torch.cuda.current_stream(self.device)
-        elif stream.device != self.device:
-            raise ValueError(f"stream is on {stream.device}, the tensors are on {self.device}")
-        self.stream = stream
-        self.ctx = torch.cuda.stream(stream)  # also makes the stream's device current
-
-    def __enter__(self):
-        self.ctx.__enter__()
-        return self.stream.cuda_stream
-
-    def __exit__(self, *exc):
-        return self.ctx.__exit__(*exc)
+        if stream is not None:
+            if stream.device.index != dev:
+                raise ValueError(f"stream is on {stream.device}, the tensors are on {t.device}")
+            with torch.cuda.stream(stream):
+                return fn(t, *args, **kw)
+        if dev != torch.cuda.current_device():
+            with torch.cuda.device(dev):
+                return fn(t, *args, **kw)
+        return fn(t, *args, **kw)
+    return call
 
 
-def _arg(t, name: str, dtype, shape) -> int | None:
+def _refuse(t, name, dtype, shape, dev):
+    if t.get_device() != dev:
+        raise ValueError(f"tensors must all be on one CUDA device ({name} is on {t.device})")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _arg(t, name: str, dtype, shape, dev: int) -> int | None:
     """Pointer of a contiguous tensor of this type and shape (None passes)."""
     if t is None:
         return None
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
-    return _ptr(t)
+    if (t.get_device() != dev or t.dtype is not dtype or t.shape != shape
+            or not t.is_contiguous()):
+        _refuse(t, name, dtype, shape, dev)
+    return t.data_ptr()
 
 
-def _strided(t, name: str, dtype, shape):
-    """Pointer and element strides {batch, head, token} of a tensor whose rows
-    are contiguous."""
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
-    if t.stride(-1) != 1:
+def _strided(t, name: str, dtype, shape, dev: int):
+    """Pointer and element strides {batch, head, token} (None: contiguous) of a
+    tensor whose rows are contiguous."""
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape:
+        _refuse(t, name, dtype, shape, dev)
+    if t.is_contiguous():
+        return t.data_ptr(), None
+    s = t.stride()
+    if s[3] != 1:
         raise ValueError(f"the rows of {name} must be contiguous")
-    return t.data_ptr(), (ctypes.c_int64 * 3)(*t.stride()[:3])
+    return t.data_ptr(), (ctypes.c_int64 * 3)(s[0], s[1], s[2])
 
 
+@_placed
 def sas_rotary(q, inv_freq, k=None, pos=None, start=None, parents=None, interleaved: bool = False,
-               amplitude: float = 1.0, inverse: bool = False, out=None, stream=None):
+               amplitude: float = 1.0, inverse: bool = False, out=None):
     """Rotary positions of q [B][Hq][N][d] and k [B][Hkv][N][d]; returns qo, or (qo, ko).
 
     q and k may be strided views (a fused projection's) with contiguous rows.
@@ -538,61 +559,59 @@ def sas_rotary(q, inv_freq, k=None, pos=None, start=None, parents=None, interlea
     transpose: it takes the gradients of the outputs to those of the inputs.
     out: qo, or (qo, ko); q and k themselves rotate in place.
     """
-    B, Hq, N, d = q.shape
-    Hkv = 0 if k is None else k.shape[1]
-    _dt(q)
-    with _On(stream, q, k, inv_freq, pos, start, parents) as st:
-        if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            if k is not None:
-                out = (out, torch.empty(k.shape, dtype=k.dtype, device=k.device))
+    B, Hq, N, d = shape = q.shape
+    dev, dtype, i32 = q.get_device(), q.dtype, torch.int32
+    dt = _dt(q)
+    if out is None:
+        qo, ko = _like(q), None if k is None else _like(k)
+    else:
         qo, ko = (out, None) if k is None else out
-        if any(t is not None and t.device != q.device for t in (qo, ko)):
-            raise ValueError("tensors must all be on one CUDA device")
-        pq, sq = _strided(q, "q", q.dtype, (B, Hq, N, d))
-        pqo, sqo = _strided(qo, "qo", q.dtype, (B, Hq, N, d))
-        pk = sk = pko = sko = None
-        if k is not None:
-            pk, sk = _strided(k, "k", q.dtype, (B, Hkv, N, d))
-            pko, sko = _strided(ko, "ko", q.dtype, (B, Hkv, N, d))
-        _check("sas_rotary", load_library().sas_rotary(
-            pq, sq, pqo, sqo, Hq, pk, sk, pko, sko, Hkv, _dt(q), B, N, d,
-            _arg(inv_freq, "inv_freq", torch.float32, (inv_freq.numel(),)), 2 * inv_freq.numel(),
-            int(bool(interleaved)), float(amplitude), int(bool(inverse)),
-            _arg(pos, "pos", torch.int32, (B, N)), _arg(start, "start", torch.int32, (B,)),
-            _arg(parents, "parents", torch.int32, (B, N)), st))
-    return out
+    pq, sq = _strided(q, "q", dtype, shape, dev)
+    pqo, sqo = _strided(qo, "qo", dtype, shape, dev)
+    Hkv = 0
+    pk = sk = pko = sko = None
+    if k is not None:
+        Hkv = k.shape[1]
+        shape = (B, Hkv, N, d)
+        pk, sk = _strided(k, "k", dtype, shape, dev)
+        pko, sko = _strided(ko, "ko", dtype, shape, dev)
+    half = inv_freq.numel()
+    _check("sas_rotary", load_library().sas_rotary(
+        pq, sq, pqo, sqo, Hq, pk, sk, pko, sko, Hkv, dt, B, N, d,
+        _arg(inv_freq, "inv_freq", torch.float32, (half,), dev), 2 * half, interleaved, amplitude,
+        inverse, _arg(pos, "pos", i32, (B, N), dev), _arg(start, "start", i32, (B,), dev),
+        _arg(parents, "parents", i32, (B, N), dev), _raw_stream(dev)))
+    return qo if k is None else (qo, ko)
 
 
-def sas_page_map(lens, nnew, block_table, free_pages, free_head, T: int, npages: int, out=None,
-                 stream=None):
+@_placed
+def sas_page_map(lens, nnew, block_table, free_pages, free_head, T: int, npages: int, out=None):
     """Pages and slots of nnew [B] <= T new tokens after lens [B] cached ones.
 
     Takes pages from free_pages[free_head:] into block_table [B][width] (in
     place) and returns (slots [B][T], new_lens [B], taken [B], head [1]), all
     int32. out supplies the four; new_lens may be lens and head free_head.
     """
-    i32 = torch.int32
-    (B,), width, nfree = lens.shape, block_table.shape[1], free_pages.numel()
-    with _On(stream, lens, nnew, block_table, free_pages, free_head, *(out or ())) as st:
-        if out is None:
-            new = dict(dtype=i32, device=lens.device)
-            out = (torch.empty((B, T), **new), torch.empty(B, **new), torch.empty(B, **new),
-                   torch.empty(1, **new))
-        slots, new_lens, taken, head = out
-        _check("sas_page_map", load_library().sas_page_map(
-            _arg(lens, "lens", i32, (B,)), _arg(nnew, "nnew", i32, (B,)),
-            _arg(block_table, "block_table", i32, (B, width)),
-            _arg(free_pages, "free_pages", i32, (nfree,)),
-            _arg(free_head, "free_head", i32, (1,)), B, T, width, npages, nfree,
-            _arg(slots, "slots", i32, (B, T)), _arg(new_lens, "new_lens", i32, (B,)),
-            _arg(taken, "taken", i32, (B,)), _arg(head, "head", i32, (1,)), st))
+    i32, dev = torch.int32, lens.get_device()
+    B, width, nfree = lens.shape[0], block_table.shape[1], free_pages.numel()
+    if out is None:
+        out = (lens.new_empty((B, T)), _like(lens), _like(lens), _like(free_head))
+    slots, new_lens, taken, head = out
+    _check("sas_page_map", load_library().sas_page_map(
+        _arg(lens, "lens", i32, (B,), dev), _arg(nnew, "nnew", i32, (B,), dev),
+        _arg(block_table, "block_table", i32, (B, width), dev),
+        _arg(free_pages, "free_pages", i32, (nfree,), dev),
+        _arg(free_head, "free_head", i32, (1,), dev), B, T, width, npages, nfree,
+        _arg(slots, "slots", i32, (B, T), dev), _arg(new_lens, "new_lens", i32, (B,), dev),
+        _arg(taken, "taken", i32, (B,), dev), _arg(head, "head", i32, (1,), dev),
+        _raw_stream(dev)))
     return out
 
 
+@_placed
 def sas_cache_append(k, v, lens, kc, vc, ksum=None, ntok=None, rows=None, slots=None,
                      inv_freq=None, interleaved: bool = False, amplitude: float = 1.0, q=None,
-                     out=None, stream=None):
+                     out=None):
     """Write new tokens' k, v [B][Hkv][T][d] into a cache, in place.
 
     The cache is kc, vc [B][Hkv][Lmax][d], or with slots [B][T] the pools
@@ -602,42 +621,44 @@ def sas_cache_append(k, v, lens, kc, vc, ksum=None, ntok=None, rows=None, slots=
     With inv_freq, k is rotated at its position first, and q [B][Hq][T][d],
     when given, beside it: returns qo (out supplies it), else None.
     """
-    i32 = torch.int32
-    B, Hkv, T, d = k.shape
-    lib, dt = load_library(), _dt(k)
-    with _On(stream, k, v, lens, kc, vc, ksum, ntok, rows, slots, inv_freq, q, out) as st:
-        if slots is None:
-            N, npages = kc.shape[2], 0
-            cshape, sshape = (B, Hkv, N, d), (B, Hkv, N // 64, d)
-        else:
-            N, npages = 0, kc.shape[0]
-            cshape, sshape = (npages, Hkv, 64, d), (npages, Hkv, d)
-        pq = sq = None
-        Hq = Hkv
-        if q is not None:
-            Hq = q.shape[1]
-            pq, sq = _strided(q, "q", k.dtype, (B, Hq, T, d))
-            if out is None:
-                out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        elif out is not None:
-            raise ValueError("out goes with q")
-        pk, sk = _strided(k, "k", k.dtype, (B, Hkv, T, d))
-        pv, sv = _strided(v, "v", k.dtype, (B, Hkv, T, d))
-        nf = 0 if inv_freq is None else inv_freq.numel()
-        _check("sas_cache_append", lib.sas_cache_append(
-            pq, sq, _arg(out, "out", k.dtype, (B, Hq, T, d)), pk, sk, pv, sv, dt, B, Hq, Hkv, T,
-            d, _arg(rows, "rows", i32, (B, T)), _arg(lens, "lens", i32, (B,)),
-            _arg(ntok, "ntok", i32, (B,)), _arg(inv_freq, "inv_freq", torch.float32, (nf,)),
-            2 * nf, int(bool(interleaved)), float(amplitude), _arg(slots, "slots", i32, (B, T)),
-            _arg(kc, "kc", k.dtype, cshape), _arg(vc, "vc", k.dtype, cshape), N, npages,
-            None if ksum is None else _arg(ksum, "ksum", ksum.dtype, sshape),
-            SAS_F32 if ksum is None else _dt(ksum), st))
+    B, Hkv, T, d = shape = k.shape
+    dev, dtype, i32 = k.get_device(), k.dtype, torch.int32
+    dt = _dt(k)
+    if slots is None:
+        N, npages = kc.shape[2], 0
+        cshape, sshape = (B, Hkv, N, d), (B, Hkv, N // 64, d)
+    else:
+        N, npages = 0, kc.shape[0]
+        cshape, sshape = (npages, Hkv, 64, d), (npages, Hkv, d)
+    pq = sq = po = None
+    Hq = Hkv
+    if q is not None:
+        Hq = q.shape[1]
+        qshape = (B, Hq, T, d)
+        pq, sq = _strided(q, "q", dtype, qshape, dev)
+        if out is None:
+            out = _like(q)
+        po = _arg(out, "out", dtype, qshape, dev)
+    elif out is not None:
+        raise ValueError("out goes with q")
+    pk, sk = _strided(k, "k", dtype, shape, dev)
+    pv, sv = _strided(v, "v", dtype, shape, dev)
+    half = 0 if inv_freq is None else inv_freq.numel()
+    _check("sas_cache_append", load_library().sas_cache_append(
+        pq, sq, po, pk, sk, pv, sv, dt, B, Hq, Hkv, T, d, _arg(rows, "rows", i32, (B, T), dev),
+        _arg(lens, "lens", i32, (B,), dev), _arg(ntok, "ntok", i32, (B,), dev),
+        _arg(inv_freq, "inv_freq", torch.float32, (half,), dev), 2 * half, interleaved, amplitude,
+        _arg(slots, "slots", i32, (B, T), dev), _arg(kc, "kc", dtype, cshape, dev),
+        _arg(vc, "vc", dtype, cshape, dev), N, npages,
+        None if ksum is None else _arg(ksum, "ksum", ksum.dtype, sshape, dev),
+        SAS_F32 if ksum is None else _dt(ksum), _raw_stream(dev)))
     return out
 
 
+@_placed
 def sas_decode_tree(q, kd, vd, kc, vc, lens, ksum, topk: int, parents=None, ntok=None,
                     block_table=None, gated: int = 1, scale: float = 0.0, out=None, idx_out=None,
-                    ws=None, stream=None):
+                    ws=None):
     """Decode of a tree of drafted tokens: q [B][Hq][T][d], kd, vd [B][Hkv][T][d]
     over caches as sas_decode's (or, with block_table, sas_decode_paged's) ->
     o [B][Hq][T][d].
@@ -646,32 +667,33 @@ def sas_decode_tree(q, kd, vd, kc, vc, lens, ksum, topk: int, parents=None, ntok
     (a chain if None). ntok [B] counts the drafted tokens (all T if None); rows
     from ntok on are left as they were in out and idx_out [B][Hkv][T][topk].
     """
-    i32 = torch.int32
-    B, Hq, T, d = q.shape
+    B, Hq, T, d = shape = q.shape
     Hkv = kd.shape[1]
+    dev, dtype, i32 = q.get_device(), q.dtype, torch.int32
     lib, dt = load_library(), _dt(q)
-    with _On(stream, q, kd, vd, kc, vc, lens, ksum, parents, ntok, block_table, out, idx_out,
-             ws) as st:
-        if block_table is None:
-            N, npages = kc.shape[2], 0
-            cshape, sshape = (B, Hkv, N, d), (B, Hkv, N // 64, d)
-        else:
-            N, npages = 64 * block_table.shape[1], kc.shape[0]
-            cshape, sshape = (npages, Hkv, 64, d), (npages, Hkv, d)
-        if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        need = lib.sas_decode_tree_workspace_size(B, Hq, Hkv, T, N, d, topk, dt)
-        w = _ws(need, q.device, ws)
-        _check("sas_decode_tree", lib.sas_decode_tree(
-            _arg(q, "q", q.dtype, (B, Hq, T, d)), _arg(kd, "kd", q.dtype, (B, Hkv, T, d)),
-            _arg(vd, "vd", q.dtype, (B, Hkv, T, d)), _arg(kc, "kc", q.dtype, cshape),
-            _arg(vc, "vc", q.dtype, cshape), dt, B, Hq, Hkv, T, N, d,
-            _arg(parents, "parents", i32, (B, T)), _arg(ntok, "ntok", i32, (B,)),
-            _arg(lens, "lens", i32, (B,)),
-            None if ksum is None else _arg(ksum, "ksum", ksum.dtype, sshape),
-            SAS_F32 if ksum is None else _dt(ksum),
-            _arg(block_table, "block_table", i32, (B, N // 64)), npages, topk, int(gated),
-            float(scale), _arg(out, "out", q.dtype, (B, Hq, T, d)),
-            _arg(idx_out, "idx_out", i32, (B, Hkv, T, topk)) if topk else None, _ptr(w),
-            w.numel() * w.element_size(), st))
+    if block_table is None:
+        N, npages = kc.shape[2], 0
+        cshape, sshape = (B, Hkv, N, d), (B, Hkv, N // 64, d)
+    else:
+        N, npages = 64 * block_table.shape[1], kc.shape[0]
+        cshape, sshape = (npages, Hkv, 64, d), (npages, Hkv, d)
+    if out is None:
+        out = _like(q)
+    need = lib.sas_decode_tree_workspace_size(B, Hq, Hkv, T, N, d, topk, dt)
+    if ws is None or ws.numel() * ws.element_size() < need:
+        ws = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    dshape = (B, Hkv, T, d)
+    _check("sas_decode_tree", lib.sas_decode_tree(
+        _arg(q, "q", dtype, shape, dev), _arg(kd, "kd", dtype, dshape, dev),
+        _arg(vd, "vd", dtype, dshape, dev), _arg(kc, "kc", dtype, cshape, dev),
+        _arg(vc, "vc", dtype, cshape, dev), dt, B, Hq, Hkv, T, N, d,
+        _arg(parents, "parents", i32, (B, T), dev), _arg(ntok, "ntok", i32, (B,), dev),
+        _arg(lens, "lens", i32, (B,), dev),
+        None if ksum is None else _arg(ksum, "ksum", ksum.dtype, sshape, dev),
+        SAS_F32 if ksum is None else _dt(ksum),
+        _arg(block_table, "block_table", i32, (B, N // 64), dev), npages, topk, gated, scale,
+        _arg(out, "out", dtype, shape, dev),
+        _arg(idx_out, "idx_out", i32, (B, Hkv, T, topk), dev) if topk else None,
+        _arg(ws, "ws", ws.dtype, ws.shape, dev), ws.numel() * ws.element_size(),
+        _raw_stream(dev)))
     return out
