@@ -43,23 +43,28 @@ __global__ void __launch_bounds__(TA_THREADS) k_tree_attn_simt(TreeArgs a, TreeW
   const int split = blockIdx.x % a.ns, tile = blockIdx.x / a.ns;
   const int G = a.Hq / a.Hkv;
   const size_t group = (size_t)b * a.Hkv + r;
-  const TreeSeq s = tree_seq(a, b, nullptr);
+  const TreeSeq s = tree_load(a, b, tree, nullptr);
+  // without selection this kernel is the call's first: it waits before it lets
+  // the next one start
+  if (a.topk == 0) grid_dep_wait();
+  grid_dep_launch();
   const int rows = G * s.nt, row0 = tile * TA_ROWS;
-  if (row0 >= rows) return;
-  tree_masks(a, b, s.nt, tree, nullptr);
+  if (row0 >= rows) {
+    grid_dep_wait();
+    return;
+  }
+  const unsigned long long early_tok = tree_early(tree);
+  const float* q = static_cast<const float*>(a.q);
+  for (int e = tid; e < TA_ROWS * D / 4; e += TA_THREADS) {
+    const int i = e / (D / 4), row = min(row0 + i, rows - 1), c = (e % (D / 4)) * 4;
+    cp_async16(qs + i * D + c,
+               q + (((size_t)b * a.Hq + r * G + row / s.nt) * a.T + row % s.nt) * D + c,
+               row0 + i < rows);
+  }
+  grid_dep_wait();
   int u0, u1;
   const int nu = tree_units<TA_THREADS>(a, w.ubits + group * a.words, bits, warp_s, &start_s,
                                         split, u0, u1);
-  const unsigned long long early_tok = tree_early(tree, s);
-  const float* q = static_cast<const float*>(a.q);
-  for (int e = tid; e < TA_ROWS * D / 4; e += TA_THREADS) {
-    const int row = row0 + e / (D / 4), c = (e % (D / 4)) * 4;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (row < rows)
-      x = *reinterpret_cast<const float4*>(
-          q + (((size_t)b * a.Hq + r * G + row / s.nt) * a.T + row % s.nt) * D + c);
-    *reinterpret_cast<float4*>(qs + (e / (D / 4)) * D + c) = x;
-  }
   float m[TA_WROWS], l[TA_WROWS], acc[TA_WROWS][E];
   TreeRow info[TA_WROWS];
   int tok[TA_WROWS];
@@ -96,16 +101,13 @@ __global__ void __launch_bounds__(TA_THREADS) k_tree_attn_simt(TreeArgs a, TreeW
       vp = static_cast<const float*>(a.vd) + group * a.T * D;
     }
     __syncthreads();  // the previous unit's tiles are read
+#pragma unroll 4
     for (int e = tid; e < SAS_BLOCK * D / 4; e += TA_THREADS) {
-      const int row = e / (D / 4), c = (e % (D / 4)) * 4;
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-      if (row < nk) {
-        x = __ldg(reinterpret_cast<const float4*>(kp + (size_t)row * D + c));
-        y = __ldg(reinterpret_cast<const float4*>(vp + (size_t)row * D + c));
-      }
-      *reinterpret_cast<float4*>(ks + row * LD + c) = x;
-      *reinterpret_cast<float4*>(vs + row * D + c) = y;
+      const int row = e / (D / 4), c = (e % (D / 4)) * 4, from = min(row, nk - 1);
+      cp_async16(ks + row * LD + c, kp + (size_t)from * D + c, row < nk);
+      cp_async16(vs + row * D + c, vp + (size_t)from * D + c, row < nk);
     }
+    cp_async_wait();
     __syncthreads();
     float z[TA_WROWS][2];
 #pragma unroll
@@ -127,7 +129,7 @@ __global__ void __launch_bounds__(TA_THREADS) k_tree_attn_simt(TreeArgs a, TreeW
       float bias[2] = {-INFINITY, -INFINITY};
       if (row < rows) {
         if (u < nu) {
-          const float sc = w.scores[(group * a.T + tok[i]) * (a.N / SAS_BLOCK) + blk];
+          const float sc = __ldcg(w.scores + (group * a.T + tok[i]) * (a.N / SAS_BLOCK) + blk);
           bias[0] = bias[1] = tree_bias(info[i], sc, blk, a.gated) * LOG2E;
         } else {
 #pragma unroll
@@ -162,6 +164,7 @@ __global__ void __launch_bounds__(TA_THREADS) k_tree_attn_simt(TreeArgs a, TreeW
       }
     }
   }
+  cp_async_wait();  // a split without units leaves no copy in flight
 #pragma unroll
   for (int i = 0; i < TA_WROWS; ++i) {
     const int row = row0 + wid * TA_WROWS + i;
@@ -176,57 +179,76 @@ __global__ void __launch_bounds__(TA_THREADS) k_tree_attn_simt(TreeArgs a, TreeW
 }
 
 // Joins the splits: o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s, one
-// warp per row. A split that saw none of a row's keys has l = 0 and wrote no
-// partial output.
+// warp per row, lane s holding split s's maximum and sum (at most 32 splits).
+// A split that saw none of a row's keys has l = 0, and its partial output is
+// not read. Latency bounds it: the partial outputs are loaded eight at a time.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) k_tree_join(TreeArgs a, TreeWs w) {
   constexpr int E = D / 32;
   const int b = blockIdx.z, r = blockIdx.y, lane = threadIdx.x & 31;
   const int G = a.Hq / a.Hkv, row = blockIdx.x * 8 + (threadIdx.x >> 5);
-  const TreeSeq s = tree_seq(a, b, nullptr);
-  if (row >= G * s.nt) return;
+  const int nt = min(max(a.ntok ? __ldg(a.ntok + b) : a.T, 0), a.T);
+  grid_dep_wait();
+  if (row >= G * nt) return;
   const size_t group = (size_t)b * a.Hkv + r, R = (size_t)G * a.T;
   const size_t at0 = group * a.ns * R + row;
-  float M = -INFINITY;
-  for (int i = lane; i < a.ns; i += 32) {
-    const float2 ml = w.ml[at0 + i * R];
-    if (ml.y != 0.f) M = fmaxf(M, ml.x);
-  }
-  M = warp_max(M);
-  float L = 0.f, acc[E];
+  float2 ml = make_float2(-1e30f, 0.f);
+  if (lane < a.ns) ml = __ldcg(w.ml + at0 + lane * R);
+  const bool seen = ml.y != 0.f;
+  const float M = warp_max(seen ? ml.x : -INFINITY);
+  const float f = seen ? exp2f(ml.x - M) : 0.f;
+  const float L = warp_sum(seen ? ml.y * f : 0.f);
+  const unsigned live = __ballot_sync(0xffffffffu, seen);
+  float acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  for (int i = 0; i < a.ns; ++i) {
-    const float2 ml = w.ml[at0 + i * R];
-    if (ml.y == 0.f) continue;
-    const float f = exp2f(ml.x - M);
-    L = fmaf(ml.y, f, L);
+  const float* src = w.part + at0 * D + lane * E;
+  for (int i0 = 0; i0 < a.ns; i0 += 8) {
+    float x[8][E];
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-      acc[e] = fmaf(w.part[(at0 + i * R) * D + lane * E + e], f, acc[e]);
+    for (int i = 0; i < 8; ++i) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[i][e] = 0.f;
+      if (live >> (i0 + i) & 1u) {
+        const float* p = src + (size_t)(i0 + i) * R * D;
+        if constexpr (E == 4) {
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(p));
+          x[i][0] = v.x; x[i][1] = v.y; x[i][2] = v.z; x[i][3] = v.w;
+        } else {
+          const float2 v = __ldcg(reinterpret_cast<const float2*>(p));
+          x[i][0] = v.x; x[i][1] = v.y;
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float fi = __shfl_sync(0xffffffffu, f, i0 + i);
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(x[i][e], fi, acc[e]);
+    }
   }
   T* o = static_cast<T*>(a.o) +
-         (((size_t)b * a.Hq + r * G + row / s.nt) * a.T + row % s.nt) * D + lane * E;
+         (((size_t)b * a.Hq + r * G + row / nt) * a.T + row % nt) * D + lane * E;
+  const float inv = 1.0f / L;
 #pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = from_f<T>(acc[e] / L);
+  for (int e = 0; e < E; e += 2) {
+    if constexpr (sizeof(T) == 2)
+      *reinterpret_cast<__nv_bfloat162*>(o + e) =
+          __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
+    else
+      *reinterpret_cast<float2*>(o + e) = make_float2(acc[e] * inv, acc[e + 1] * inv);
+  }
 }
 
 // ------------------------------------------------------------------ host
 cudaError_t launch_tree_join(const TreeArgs& a, const TreeWs& w, int bf16, int d,
                              cudaStream_t st) {
   const dim3 grid((a.Hq / a.Hkv * a.T + 7) / 8, a.Hkv, a.B);
-  if (bf16) {
-    if (d == 128)
-      k_tree_join<__nv_bfloat16, 128><<<grid, 256, 0, st>>>(a, w);
-    else
-      k_tree_join<__nv_bfloat16, 64><<<grid, 256, 0, st>>>(a, w);
-  } else {
-    if (d == 128)
-      k_tree_join<float, 128><<<grid, 256, 0, st>>>(a, w);
-    else
-      k_tree_join<float, 64><<<grid, 256, 0, st>>>(a, w);
-  }
-  return cudaGetLastError();
+  if (bf16)
+    return d == 128 ? tree_launch(k_tree_join<__nv_bfloat16, 128>, grid, 256, 0, st, a, w)
+                    : tree_launch(k_tree_join<__nv_bfloat16, 64>, grid, 256, 0, st, a, w);
+  return d == 128 ? tree_launch(k_tree_join<float, 128>, grid, 256, 0, st, a, w)
+                  : tree_launch(k_tree_join<float, 64>, grid, 256, 0, st, a, w);
 }
 
 template <int D>
@@ -236,8 +258,7 @@ static cudaError_t launch_simt(const TreeArgs& a, const TreeWs& w, cudaStream_t 
   cudaError_t e = ensure_smem(k_tree_attn_simt<D>, smem);
   if (e != cudaSuccess) return e;
   const int rows = a.Hq / a.Hkv * a.T, tiles = (rows + TA_ROWS - 1) / TA_ROWS;
-  k_tree_attn_simt<D><<<dim3(tiles * a.ns, a.Hkv, a.B), TA_THREADS, smem, st>>>(a, w);
-  e = cudaGetLastError();
+  e = tree_launch(k_tree_attn_simt<D>, dim3(tiles * a.ns, a.Hkv, a.B), TA_THREADS, smem, st, a, w);
   return e != cudaSuccess ? e : launch_tree_join(a, w, 0, D, st);
 }
 
@@ -245,15 +266,16 @@ cudaError_t launch_tree_attn_simt(const TreeArgs& a, const TreeWs& w, int d, cud
   return d == 128 ? launch_simt<128>(a, w, st) : launch_simt<64>(a, w, st);
 }
 
-// Splits of a kv group's units: enough CTAs for two an SM, no more than the
-// units that the tokens can select.
+// Splits of a kv group's units: as many as one wave of two CTAs an SM holds (a
+// second, shorter wave would cost another start), no more than the units that
+// the tokens can select, and at most one per lane of the join.
 int tree_splits(int B, int Hq, int Hkv, int T, int N, int topk, int bf16) {
   const int tile = bf16 ? 128 : TA_ROWS;
   const long long tiles = ((long long)(Hq / Hkv) * T + tile - 1) / tile;
   const long long ctas = tiles * Hkv * B;
   long long units = (long long)T * topk;
   if (units > N / SAS_BLOCK) units = N / SAS_BLOCK;
-  long long ns = (2 * 148 + ctas / 2) / ctas;
+  long long ns = 2 * 148 / ctas;
   if (ns > units + 2) ns = units + 2;
   if (ns > 32) ns = 32;
   return ns < 1 ? 1 : (int)ns;

@@ -100,7 +100,7 @@ __device__ __noinline__ float2 repair_row(const TreeArgs& a, const TreeWs& w, co
       if (u <= nu) {
         if (u < nu) {
           blk = u == u0 ? start : tree_next(bits, a.words, blk + 1);
-          bias = tree_bias(rs.info, w.scores[(group * a.T + rs.tok) * (a.N / SAS_BLOCK) + blk],
+          bias = tree_bias(rs.info, __ldcg(w.scores + (group * a.T + rs.tok) * (a.N / SAS_BLOCK) + blk),
                            blk, a.gated);
         } else {
           nk = s.tail;
@@ -159,14 +159,37 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
   const int split = blockIdx.x % a.ns, tile = blockIdx.x / a.ns;
   const int G = a.Hq / a.Hkv;
   const size_t group = (size_t)b * a.Hkv + r;
-  const TreeSeq s = tree_seq(a, b, nullptr);
+  const TreeSeq s = tree_load(a, b, tree, nullptr);
+  // without selection this kernel is the call's first: it waits before it lets
+  // the next one start
+  if (a.topk == 0) grid_dep_wait();
+  grid_dep_launch();
   const int rows = G * s.nt, row0 = tile * 128;
-  if (row0 >= rows) return;
-  if ((smem_u32(sm) & 1023u) != 0) {  // swizzled tiles need 1024-byte alignment
-    if (tid == 0) atomicOr(err, kErrBadIndex);
+  if (row0 >= rows) {
+    grid_dep_wait();
     return;
   }
-  tree_masks(a, b, s.nt, tree, nullptr);
+  if ((smem_u32(sm) & 1023u) != 0) {  // swizzled tiles need 1024-byte alignment
+    if (tid == 0) atomicOr(err, kErrBadIndex);
+    grid_dep_wait();
+    return;
+  }
+  const int nwarp = min(4, (rows - row0 + 31) / 32);  // softmax warps with rows
+  if (tid == 0) {
+    for (int i = 0; i < NBAR; ++i) mbar_init(&bars[i], i == B_PF ? nwarp : 1);
+    fence_mbar_init();
+  }
+  if (warp == 5) tc::tmem_alloc(tmem_slot, 256);
+  // Q: rows of the group's heads, zeros behind the last (only as far as the
+  // softmax warps look; other rows' products are never read)
+  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
+  for (int e = tid; e < nwarp * 32 * PC; e += TT_THREADS) {
+    const int row = e / PC, p = e % PC, gr = min(row0 + row, rows - 1);
+    cp_async16(sm + L::Q + sw_off(row, p, 128),
+               q + (((size_t)b * a.Hq + r * G + gr / s.nt) * a.T + gr % s.nt) * D + p * 8,
+               row0 + row < rows);
+  }
+  grid_dep_wait();
   int u0, u1;
   const int nu = tree_units<TT_THREADS>(a, w.ubits + group * a.words, bits, warp_s, &start_s,
                                         split, u0, u1);
@@ -176,26 +199,6 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
   const int nsp = (int)has_tail + (int)has_draft;
   const int nh = max(0, min(u1, nu) - u0), nunits = nsp + nh;
   const size_t prow = (group * a.ns + split) * (size_t)(G * a.T) + row0 + tid;
-  if (nunits == 0) {
-    if (tid < 128 && row0 + tid < rows) w.ml[prow] = make_float2(-1e30f, 0.f);
-    return;
-  }
-  const int nwarp = min(4, (rows - row0 + 31) / 32);  // softmax warps with rows
-  if (tid == 0) {
-    for (int i = 0; i < NBAR; ++i) mbar_init(&bars[i], i == B_PF ? nwarp : 1);
-    fence_mbar_init();
-  }
-  if (warp == 5) tc::tmem_alloc(tmem_slot, 256);
-  // Q: rows of the group's heads, zeros behind the last
-  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
-  for (int e = tid; e < 128 * PC; e += TT_THREADS) {
-    const int row = e / PC, p = e % PC, gr = row0 + row;
-    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-    if (gr < rows)
-      x = __ldg(reinterpret_cast<const uint4*>(
-          q + (((size_t)b * a.Hq + r * G + gr / s.nt) * a.T + gr % s.nt) * D + p * 8));
-    *reinterpret_cast<uint4*>(sm + L::Q + sw_off(row, p, 128)) = x;
-  }
   // the units that end inside a tile
   for (int j = 0; j < nsp; ++j) {
     const bool is_tail = has_tail && j == 0;
@@ -210,22 +213,24 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
       vp = static_cast<const __nv_bfloat16*>(a.vd) + group * a.T * D;
     }
     unsigned char* st = sm + L::KV + j * 2 * L::TILE;
+#pragma unroll 2
     for (int e = tid; e < 64 * PC; e += TT_THREADS) {
-      const int row = e / PC, p = e % PC;
-      uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
-      if (row < nk) {
-        x = __ldg(reinterpret_cast<const uint4*>(kp + (size_t)row * D + p * 8));
-        y = __ldg(reinterpret_cast<const uint4*>(vp + (size_t)row * D + p * 8));
-      }
-      *reinterpret_cast<uint4*>(st + sw_off(row, p, 64)) = x;
-      *reinterpret_cast<uint4*>(st + L::TILE + sw_off(row, p, 64)) = y;
+      const int row = e / PC, p = e % PC, from = min(row, nk - 1);
+      cp_async16(st + sw_off(row, p, 64), kp + (size_t)from * D + p * 8, row < nk);
+      cp_async16(st + L::TILE + sw_off(row, p, 64), vp + (size_t)from * D + p * 8, row < nk);
     }
   }
+  cp_async_wait();
   fence_proxy_async_smem();  // the tiles above are read by the tensor cores
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
+  if (nunits == 0) {  // more splits than units
+    if (tid < 128 && row0 + tid < rows) w.ml[prow] = make_float2(-1e30f, 0.f);
+    if (warp == 5) tc::tmem_dealloc(tmem, 256);
+    return;
+  }
   const uint32_t tm_s[2] = {tmem, tmem + 64};
   const uint32_t tm_o = tmem + 128;
   const int start = nh > 0 ? start_s : 0;
@@ -307,7 +312,7 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
     RowState rs;
     rs.tok = valid ? row % s.nt : 0;
     rs.anc = tree.anc[rs.tok];
-    rs.early = tree_early(tree, s);
+    rs.early = tree_early(tree);
     rs.info = tree_row(a, w, s, group, rs.tok, rs.anc);
     const float* sc = w.scores + (group * a.T + rs.tok) * (size_t)(a.N / SAS_BLOCK);
     float m = -1e30f, l = 0.f;
@@ -315,7 +320,7 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
     float next_score = 0.f;
     if (nh > 0) {  // the score of the next history unit is loaded a unit ahead
       blk = start;
-      next_score = sc[blk];
+      next_score = __ldcg(sc + blk);
     }
     for (int j = 0; j < nunits; ++j) {
       const int st = j & 1;
@@ -330,7 +335,7 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
         bias = tree_bias(rs.info, next_score, blk, a.gated) * LOG2E;
         if (j + 1 < nunits) {
           blk = tree_next(bits, a.words, blk + 1);
-          next_score = sc[blk];
+          next_score = __ldcg(sc + blk);
         }
       }
       if (!valid) see = 0ull;
@@ -469,8 +474,8 @@ static cudaError_t launch_tc(const TreeArgs& a, const TreeWs& w, cudaStream_t st
   cudaError_t e = ensure_smem(k_tree_attn_tc<D>, smem);
   if (e != cudaSuccess) return e;
   const int rows = a.Hq / a.Hkv * a.T, tiles = (rows + 127) / 128;
-  k_tree_attn_tc<D><<<dim3(tiles * a.ns, a.Hkv, a.B), TT_THREADS, smem, st>>>(km, vm, a, w);
-  e = cudaGetLastError();
+  e = tree_launch(k_tree_attn_tc<D>, dim3(tiles * a.ns, a.Hkv, a.B), TT_THREADS, smem, st, km, vm,
+                  a, w);
   if (e != cudaSuccess) return e;
   return launch_tree_join(a, w, 1, D, st);
 }

@@ -6,8 +6,14 @@
 //   s_i,c0 with the mean of that block's 64 keys (rounded to the summaries'
 //   type); log g = s - LSE(s); the topk best, ties to the lower block.
 //
-// k_tree_scores: one CTA per (64 summaries, kv group, sequence) reads its
-// summaries once for all T tokens. k_tree_select: one CTA per row.
+// k_tree_scores reads every summary once for all T tokens. The products are
+// tensor-core work (T x C x d multiply-adds: fp32 FMAs would take 14 us at
+// 512K and T = 64, where the summaries' bytes take 5), but the order of the
+// blocks needs fp32: each factor is split into two tf32 parts, x = hi + lo + e
+// with |e| <= 2^-22 |x|, and hi hi + hi lo + lo hi is accumulated in fp32
+// (bf16 summaries are tf32 values: one part). What is dropped is 2^-22 of a
+// product, below the fp32 accumulation's own rounding.
+// k_tree_select: one CTA per row.
 #include <math.h>
 
 #include "common.cuh"
@@ -20,95 +26,150 @@ namespace sas {
 __device__ uint32_t g_tree_select_err = 0;
 
 namespace {
-constexpr int TS_THREADS = 256;
-constexpr int TS_BLOCKS = 64;  // summaries of a CTA
+
+constexpr int TS_THREADS = 128;
+constexpr int TS_BLOCKS = 16 * (TS_THREADS / 32);  // summaries of a pass: 16 a warp
+
+// D += A B, m16n8k8: A[row][k], B[k][col] in tf32 (row-major, column-major
+// fragments), D in fp32.
+__device__ __forceinline__ void mma_tf32(float (&c)[4], const float (&a)[4], float b0, float b1) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(__float_as_uint(a[0])), "r"(__float_as_uint(a[1])), "r"(__float_as_uint(a[2])),
+        "r"(__float_as_uint(a[3])), "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)));
 }
 
+// The leading 11 significant bits of x (a tf32 value), and of what is left.
+__device__ __forceinline__ float tf32_hi(float x) {
+  return __uint_as_float(__float_as_uint(x) & 0xffffe000u);
+}
+
+// Four consecutive summary elements as fp32.
+__device__ __forceinline__ void load4(const float* p, float (&x)[4]) {
+  const float4 v = __ldg(reinterpret_cast<const float4*>(p));
+  x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+}
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&x)[4]) {
+  const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+  x[0] = __uint_as_float(v.x << 16); x[1] = __uint_as_float(v.x & 0xffff0000u);
+  x[2] = __uint_as_float(v.y << 16); x[3] = __uint_as_float(v.y & 0xffff0000u);
+}
+
+}  // namespace
+
+// One CTA per (stretch of summaries, kv group, sequence). A warp multiplies 16
+// summaries (rows of A, straight from global memory) with all tokens (columns
+// of B, in shared memory, split once). The order of the k index inside a group
+// of 16 is free as long as A and B share it: lane c of a quad takes elements
+// 4c .. 4c + 3, one 16-byte load, as k = c and c + 4 of two steps. Rows of
+// shared memory are D + 16 floats apart, so that those loads meet no bank twice.
 template <typename T, typename S, int D>
-__global__ void __launch_bounds__(TS_THREADS) k_tree_scores(TreeArgs a, TreeWs w) {
-  constexpr int LD = D + 4;
+__global__ void __launch_bounds__(TS_THREADS) k_tree_scores(TreeArgs a, TreeWs w, int stretch) {
+  constexpr int LD = D + 16, VT = Vec16<T>::N, KG = D / 16;
+  constexpr bool SPLIT = sizeof(S) == 4;
   extern __shared__ __align__(16) float sm_f[];
-  float* ks = sm_f;                  // [64][LD]
-  float* qb = sm_f + TS_BLOCKS * LD;  // [64][LD]
-  const int r = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
-  const int m0 = blockIdx.x * TS_BLOCKS, G = a.Hq / a.Hkv, C = a.N / SAS_BLOCK;
+  const int T8 = (a.T + 7) & ~7;
+  float* qh = sm_f;            // [T8][LD]
+  float* ql = sm_f + T8 * LD;  // [T8][LD]
+  const int r = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int G = a.Hq / a.Hkv, C = a.N / SAS_BLOCK;
+  const int m_lo = blockIdx.x * stretch;
   const size_t group = (size_t)b * a.Hkv + r;
-  if (tid < TS_BLOCKS / 32) {
-    const int word = m0 / 32 + tid;
-    if (word < a.words) w.ubits[group * a.words + word] = 0u;
-  }
-  const TreeSeq s = tree_seq(a, b, nullptr);
-  if (m0 >= s.c0 || s.nt == 0) return;
-  constexpr int VS = Vec16<S>::N, VT = Vec16<T>::N;
-  for (int e = tid; e < TS_BLOCKS * (D / VS); e += TS_THREADS) {
-    const int row = e / (D / VS), c = (e % (D / VS)) * VS, m = m0 + row;
-    float x[VS];
-#pragma unroll
-    for (int i = 0; i < VS; ++i) x[i] = 0.f;
-    if (m < s.c0) {
-      const size_t at = a.table ? (size_t)tree_page(a, b, m, &g_tree_select_err) * a.Hkv + r
-                                : group * C + m;
-      Vec16<S>::load_nc(static_cast<const S*>(a.ksum) + at * D + c, x);
-    }
-#pragma unroll
-    for (int i = 0; i < VS; ++i) ks[row * LD + c + i] = x[i];
-  }
+  grid_dep_wait();
+  grid_dep_launch();
+  for (int i = m_lo / 32 + tid; i < min((m_lo + stretch) / 32, a.words); i += TS_THREADS)
+    w.ubits[group * a.words + i] = 0u;
+  const int n = __ldg(a.lens + b), ntk = a.ntok ? __ldg(a.ntok + b) : a.T;
+  const int c0 = min(max(n, 0), a.N) / SAS_BLOCK, nt = min(max(ntk, 0), a.T);
+  const int m_hi = min(m_lo + stretch, c0);
+  if (m_lo >= m_hi || nt == 0) return;
   const float inv_g = 1.0f / (float)G;
-  for (int e = tid; e < TREE_MAX * (D / VT); e += TS_THREADS) {
+  for (int e = tid; e < T8 * (D / VT); e += TS_THREADS) {
     const int row = e / (D / VT), c = (e % (D / VT)) * VT;
     float x[VT];
 #pragma unroll
     for (int i = 0; i < VT; ++i) x[i] = 0.f;
-    if (row < s.nt)
+    if (row < nt) {
+      const T* q = static_cast<const T*>(a.q) + (((size_t)b * a.Hq + r * G) * a.T + row) * D + c;
+#pragma unroll 4
       for (int g = 0; g < G; ++g) {
         float y[VT];
-        Vec16<T>::load_nc(static_cast<const T*>(a.q) +
-                              (((size_t)b * a.Hq + r * G + g) * a.T + row) * D + c, y);
+        Vec16<T>::load_nc(q + (size_t)g * a.T * D, y);
 #pragma unroll
         for (int i = 0; i < VT; ++i) x[i] += y[i];
       }
+    }
 #pragma unroll
-    for (int i = 0; i < VT; ++i) qb[row * LD + c + i] = x[i] * inv_g;
+    for (int i = 0; i < VT; ++i) {
+      const float m = x[i] * inv_g, h = tf32_hi(m);
+      qh[row * LD + c + i] = h;
+      ql[row * LD + c + i] = tf32_hi(m - h);
+    }
   }
   __syncthreads();
-  // 4 x 4 scores a thread: tokens ti + 16 i, blocks tj + 16 j
-  const int tj = tid & 15, ti = tid >> 4;
-  if (ti >= s.nt) return;
-  float acc[4][4];
+  const int quad = lane >> 2, c = lane & 3, ntiles = (nt + 7) >> 3;
+  for (int m0 = m_lo + wid * 16; m0 < m_hi; m0 += TS_BLOCKS) {
+    // A: rows quad and quad + 8 of the warp's 16 (a row past the end reads the last one)
+    float x[2][KG][4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+    for (int h = 0; h < 2; ++h) {
+      const int m = min(m0 + quad + 8 * h, m_hi - 1);
+      const size_t at =
+          a.table ? (size_t)tree_page(a, b, m, &g_tree_select_err) * a.Hkv + r : group * C + m;
+      const S* p = static_cast<const S*>(a.ksum) + at * D + 4 * c;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-#pragma unroll 4
-  for (int c = 0; c < D; c += 4) {
-    float4 x[4], y[4];
+      for (int g = 0; g < KG; ++g) load4(p + 16 * g, x[h][g]);
+    }
+    float acc[TREE_MAX / 8][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[i] = *reinterpret_cast<const float4*>(qb + (ti + 16 * i) * LD + c);
-      y[i] = *reinterpret_cast<const float4*>(ks + (tj + 16 * i) * LD + c);
+    for (int j = 0; j < TREE_MAX / 8; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
+#pragma unroll
+    for (int g = 0; g < KG; ++g) {
+      float hi[2][4], lo[2][4];  // of the two k steps of this group
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // fragment i: row half i & 1, k half i >> 1
+          const float v = x[i & 1][g][2 * k + (i >> 1)];
+          hi[k][i] = SPLIT ? tf32_hi(v) : v;
+          lo[k][i] = SPLIT ? tf32_hi(v - hi[k][i]) : 0.f;
+        }
+#pragma unroll
+      for (int j = 0; j < TREE_MAX / 8; ++j) {
+        if (j < ntiles) {
+          const int at = (8 * j + quad) * LD + 16 * g + 4 * c;
+          const float4 bh = *reinterpret_cast<const float4*>(qh + at);
+          const float4 bl = *reinterpret_cast<const float4*>(ql + at);
+          mma_tf32(acc[j], hi[0], bl.x, bl.y);
+          mma_tf32(acc[j], hi[1], bl.z, bl.w);
+          if (SPLIT) {
+            mma_tf32(acc[j], lo[0], bh.x, bh.y);
+            mma_tf32(acc[j], lo[1], bh.z, bh.w);
+          }
+          mma_tf32(acc[j], hi[0], bh.x, bh.y);
+          mma_tf32(acc[j], hi[1], bh.z, bh.w);
+        }
+      }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int j = 0; j < TREE_MAX / 8; ++j)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        acc[i][j] = fmaf(x[i].x, y[j].x, acc[i][j]);
-        acc[i][j] = fmaf(x[i].y, y[j].y, acc[i][j]);
-        acc[i][j] = fmaf(x[i].z, y[j].z, acc[i][j]);
-        acc[i][j] = fmaf(x[i].w, y[j].w, acc[i][j]);
+      for (int i = 0; i < 4; ++i) {  // row quad + 8 (i >> 1), column 2 c + (i & 1)
+        const int t = 8 * j + 2 * c + (i & 1), m = m0 + quad + 8 * (i >> 1);
+        if (t < nt && m < m_hi)
+          w.scores[(group * a.T + t) * C + m] = acc[j][i] * a.scale + 0.f;
       }
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int t = ti + 16 * i, m = m0 + tj + 16 * j;
-      if (t < s.nt && m < s.c0) w.scores[(group * a.T + t) * C + m] = acc[i][j] * a.scale + 0.f;
-    }
 }
 
 namespace {
 constexpr int SEL_THREADS = 256;
-}
+constexpr int SEL_WARPS = SEL_THREADS / 32;
+constexpr int SEL_LIST = 512;  // candidates ranked by counting
+}  // namespace
 
 __device__ __forceinline__ float block_sum(float v, float* red) {
   v = warp_sum(v);
@@ -116,45 +177,88 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
   __syncthreads();
   float t = 0.f;
 #pragma unroll
-  for (int i = 0; i < SEL_THREADS / 32; ++i) t += red[i];
-  __syncthreads();
-  return t;
-}
-__device__ __forceinline__ float block_max(float v, float* red) {
-  v = warp_max(v);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  float t = red[0];
-#pragma unroll
-  for (int i = 1; i < SEL_THREADS / 32; ++i) t = fmaxf(t, red[i]);
+  for (int i = 0; i < SEL_WARPS; ++i) t += red[i];
   __syncthreads();
   return t;
 }
 
+// The kk-th best of n keys and the last block that is kept at that key, for
+// sets with more equal or near-equal keys than the list holds: the threshold
+// bit by bit, then the keys equal to it in block order. Every thread owns the
+// stretch [lo, hi). Returns through th and last (shared).
+__device__ __noinline__ void select_by_bits(const uint32_t* keys, int lo, int hi, int kk,
+                                            uint32_t* scan, uint32_t* th_s, int* last_s) {
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  uint32_t th = 0;
+  for (int bit = 31; bit >= 0; --bit) {
+    const uint32_t cand = th | (1u << bit);
+    uint32_t c = 0;
+    for (int m = lo; m < hi; ++m) c += keys[m] >= cand;
+    c = __reduce_add_sync(0xffffffffu, c);
+    if (lane == 0) scan[wid] = c;
+    __syncthreads();
+    c = 0;
+#pragma unroll
+    for (int i = 0; i < SEL_WARPS; ++i) c += scan[i];
+    if (c >= (uint32_t)kk) th = cand;
+    __syncthreads();
+  }
+  uint32_t above = 0, equal = 0;
+  for (int m = lo; m < hi; ++m) {
+    above += keys[m] > th;
+    equal += keys[m] == th;
+  }
+  uint32_t v = (above << 16) | equal;  // both below 2^16
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += y;
+  }
+  if (lane == 31) scan[wid] = v;
+  __syncthreads();
+  uint32_t before = v - ((above << 16) | equal), all = 0;
+#pragma unroll
+  for (int i = 0; i < SEL_WARPS; ++i) {
+    before += i < wid ? scan[i] : 0u;
+    all += scan[i];
+  }
+  const int take = kk - (int)(all >> 16);  // of the keys equal to th
+  int eq = (int)(before & 0xffffu);
+  for (int m = lo; m < hi; ++m)
+    if (keys[m] == th && ++eq == take) *last_s = m;
+  if (tid == 0) *th_s = th;
+  __syncthreads();
+}
+
 template <typename T, typename S, int D>
 __global__ void __launch_bounds__(SEL_THREADS) k_tree_select(TreeArgs a, TreeWs w) {
-  extern __shared__ __align__(16) uint32_t keys[];  // (C_i) keys, thread t owns [t n, t n + n)
+  extern __shared__ __align__(16) uint32_t keys[];  // C_i keys
   __shared__ TreeShared tree;
-  __shared__ float red[SEL_THREADS / 32];
-  __shared__ uint32_t scan[SEL_THREADS / 32];
+  __shared__ float red[SEL_WARPS];
+  __shared__ uint32_t scan[SEL_WARPS];
   __shared__ float part[SEL_THREADS];
-  __shared__ int last_s;
+  __shared__ __align__(16) unsigned long long list[SEL_LIST];
+  __shared__ int kept[128];
+  __shared__ int cnt_s, last_s;
+  __shared__ uint32_t th_s;
   const int i = blockIdx.x, r = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
-  if (tid == 0) last_s = -1;
+  const int lane = tid & 31, wid = tid >> 5;
+  grid_dep_launch();
   const int C = a.N / SAS_BLOCK, G = a.Hq / a.Hkv;
   const size_t group = (size_t)b * a.Hkv + r, row = group * a.T + i;
-  const TreeSeq s = tree_seq(a, b, (i == 0 && r == 0) ? &g_tree_select_err : nullptr);
-  if (i >= s.nt) return;
-  tree_masks(a, b, s.nt, tree, (i == 0 && r == 0) ? &g_tree_select_err : nullptr);
+  const TreeSeq s = tree_load(a, b, tree, (i == 0 && r == 0) ? &g_tree_select_err : nullptr);
+  if (i >= s.nt) {
+    grid_dep_wait();
+    return;
+  }
   const unsigned long long anc = tree.anc[i];
-  const int depth = tree_depth(anc);
-  const bool crossed = s.tail + depth >= SAS_BLOCK;
+  const bool crossed = s.tail + tree_depth(anc) >= SAS_BLOCK;
   const int Ci = s.c0 + (crossed ? 1 : 0);
   const int kk = min(a.topk, Ci);
   float virt = 0.f;
   if (crossed) {
-    // mean key of the tail's block as this path fills it: thread (half, column)
-    // sums every second key, tail keys first, then the path's in their order
+    // mean key of the tail's block as this path fills it: thread (part, column)
+    // sums every P-th key, the tail's first, then the path's in their order
     constexpr int P = SEL_THREADS / D;
     const int c = tid % D, p = tid / D;
     const T* kc = static_cast<const T*>(a.kc);
@@ -162,6 +266,7 @@ __global__ void __launch_bounds__(SEL_THREADS) k_tree_select(TreeArgs a, TreeWs 
     float sum = 0.f;
     if (s.tail > 0) {
       const size_t base = tree_block_row(a, b, r, s.c0, &g_tree_select_err);
+#pragma unroll 8
       for (int j = p; j < s.tail; j += P) sum += to_f(kc[(base + j) * D + c]);
     }
     unsigned long long rest = anc;
@@ -185,74 +290,107 @@ __global__ void __launch_bounds__(SEL_THREADS) k_tree_select(TreeArgs a, TreeWs 
     }
     virt = block_sum(dot, red) * a.scale;
   }
-  // each thread owns a stretch of n (odd: no bank conflicts) blocks
-  const int n = ((Ci + SEL_THREADS - 1) / SEL_THREADS) | 1;
+  if (tid == 0) {
+    cnt_s = 0;
+    last_s = -1;
+    th_s = 0xffffffffu;
+  }
+  grid_dep_wait();
   const float* sc = w.scores + row * C;
   float mx = -INFINITY;
+  uint32_t best = 0;  // below every key of a finite score
+#pragma unroll 8
   for (int m = tid; m < Ci; m += SEL_THREADS) {
-    const float v = m < s.c0 ? sc[m] : virt;
-    keys[m] = score_key(v);
+    const float v = m < s.c0 ? __ldcg(sc + m) : virt;
+    const uint32_t key = score_key(v);
+    keys[m] = key;
+    best = max(best, key);
     mx = fmaxf(mx, v);
   }
-  mx = block_max(mx, red);
-  const int lo = min(tid * n, Ci), hi = min(lo + n, Ci);
+  mx = warp_max(mx);
+  if (lane == 0) red[wid] = mx;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < SEL_WARPS; ++k) mx = fmaxf(mx, red[k]);
+  // A lower bound of the kk-th best key: that of the threads' own best ones (a
+  // subset), by its upper 16 bits.
+  uint32_t bound = 0;
+#pragma unroll 1
+  for (int bit = 31; bit >= 16; --bit) {
+    const uint32_t cand = bound | (1u << bit);
+    if (__syncthreads_count(best >= cand) >= kk) bound = cand;
+  }
   float sum = 0.f;
-  for (int m = lo; m < hi; ++m) sum += expf(score_of(keys[m]) - mx);
-  const float lse = mx + logf(block_sum(sum, red));
-  // k-th largest key by bits, from the top: the largest th with at least kk keys >= th
-  uint32_t th = 0;
-  if (kk > 0) {
-    for (int bit = 31; bit >= 0; --bit) {
-      const uint32_t cand = th | (1u << bit);
-      int c = 0;
-      for (int m = lo; m < hi; ++m) c += keys[m] >= cand;
-      c = (int)block_sum((float)c, red);
-      if (c >= kk) th = cand;
+  for (int m0 = 0; m0 < Ci; m0 += SEL_THREADS) {
+    const int m = m0 + tid;
+    const uint32_t key = m < Ci ? keys[m] : 0u;
+    if (m < Ci) sum += expf(score_of(key) - mx);
+    const bool keep = m < Ci && key >= bound;
+    const unsigned mask = __ballot_sync(0xffffffffu, keep);
+    if (mask) {
+      int base = 0;
+      if (lane == 0) base = atomicAdd(&cnt_s, __popc(mask));
+      base = __shfl_sync(0xffffffffu, base, 0) + __popc(mask & ((1u << lane) - 1u));
+      if (keep && base < SEL_LIST)
+        list[base] = ((unsigned long long)key << 32) | (0xffffffffu - (uint32_t)m);
     }
   }
-  // keys above th are kept; of those equal to it the first ones, in block order
-  uint32_t above = 0, equal = 0;
-  for (int m = lo; m < hi; ++m) {
-    above += keys[m] > th;
-    equal += keys[m] == th;
-  }
-  uint32_t v = (above << 16) | equal;  // both below 2^16
-  const int lane = tid & 31, wid = tid >> 5;
+  const float lse = mx + logf(block_sum(sum, red));  // its barriers also close the list
+  const int n = cnt_s;
+  if (kk > 0 && n <= SEL_LIST) {
+    // unique keys: a candidate's rank is the number of larger ones
+    for (int e = tid; e < n; e += SEL_THREADS) {
+      const unsigned long long key = list[e];
+      const int rank = count_above(list, n, key);
+      if (rank < kk) {
+        const int m = key_block(key);
+        kept[rank] = m;
+        if (m < s.c0) atomicOr(&w.ubits[group * a.words + (m >> 5)], 1u << (m & 31));
+        if (rank == kk - 1) {
+          th_s = (uint32_t)(key >> 32);
+          last_s = m;
+        }
+      }
+    }
+    __syncthreads();
+    if (a.idx_out && tid < kk) {  // ascending: a block's place is the number of smaller ones
+      const int m = kept[tid];
+      int at = 0;
+      for (int e = 0; e < kk; ++e) at += kept[e] < m;
+      a.idx_out[row * a.topk + at] = m;
+    }
+  } else if (kk > 0) {
+    const int per = ((Ci + SEL_THREADS - 1) / SEL_THREADS) | 1;  // odd: no bank conflicts
+    const int lo = min(tid * per, Ci), hi = min(lo + per, Ci);
+    select_by_bits(keys, lo, hi, kk, scan, &th_s, &last_s);
+    const uint32_t th = th_s;
+    const int last = last_s;
+    // places by counting the kept blocks of the earlier threads
+    uint32_t mine = 0;
+    for (int m = lo; m < hi; ++m) mine += keys[m] > th || (keys[m] == th && m <= last);
+    uint32_t v = mine;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t y = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += y;
-  }
-  if (lane == 31) scan[wid] = v;
-  __syncthreads();
-  uint32_t before = v - ((above << 16) | equal), all = 0;
-#pragma unroll
-  for (int k = 0; k < SEL_THREADS / 32; ++k) {
-    before += k < wid ? scan[k] : 0u;
-    all += scan[k];
-  }
-  const int take = kk - (int)(all >> 16);  // of the keys equal to th
-  int eq = (int)(before & 0xffffu);
-  int at = (int)(before >> 16) + min(eq, take);
-  if (kk > 0)
-    for (int m = lo; m < hi; ++m) {
-      const uint32_t key = keys[m];
-      const bool keep = key > th || (key == th && eq < take);
-      eq += key == th;
-      if (key == th && eq == take) last_s = m;
-      if (keep && at < kk) {
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += y;
+    }
+    if (lane == 31) scan[wid] = v;
+    __syncthreads();
+    int at = (int)(v - mine);
+    for (int k = 0; k < wid; ++k) at += scan[k];
+    for (int m = lo; m < hi; ++m)
+      if ((keys[m] > th || (keys[m] == th && m <= last)) && at < kk) {
         if (a.idx_out) a.idx_out[row * a.topk + at] = m;
         if (m < s.c0) atomicOr(&w.ubits[group * a.words + (m >> 5)], 1u << (m & 31));
         ++at;
       }
-    }
+  }
   if (a.idx_out)
     for (int p = kk + tid; p < a.topk; p += SEL_THREADS) a.idx_out[row * a.topk + p] = -1;
-  __syncthreads();
   if (tid == 0) {
     TreeRow t;
     t.lse = lse;
-    t.th = kk > 0 ? th : 0xffffffffu;
+    t.th = th_s;
     t.last = last_s;
     t.tail_bias = 0.f;
     if (crossed) t.tail_bias = kk > 0 ? tree_bias(t, virt, s.c0, a.gated) : -INFINITY;
@@ -263,19 +401,21 @@ __global__ void __launch_bounds__(SEL_THREADS) k_tree_select(TreeArgs a, TreeWs 
 // ------------------------------------------------------------------ host
 template <typename T, typename S, int D>
 static cudaError_t launch_typed(const TreeArgs& a, const TreeWs& w, cudaStream_t st) {
-  const int C = a.N / SAS_BLOCK;
-  const size_t smem = (size_t)(TS_BLOCKS + TREE_MAX) * (D + 4) * sizeof(float);
+  const int C = a.N / SAS_BLOCK, T8 = (a.T + 7) & ~7;
+  const size_t smem = (size_t)2 * T8 * (D + 16) * sizeof(float);
   cudaError_t e = ensure_smem(k_tree_scores<T, S, D>, smem);
   if (e != cudaSuccess) return e;
   const size_t ksm = (size_t)(C + 1) * sizeof(uint32_t);
   e = ensure_smem(k_tree_select<T, S, D>, ksm);
   if (e != cudaSuccess) return e;
-  k_tree_scores<T, S, D><<<dim3((C + TS_BLOCKS - 1) / TS_BLOCKS, a.Hkv, a.B), TS_THREADS, smem,
-                           st>>>(a, w);
-  e = cudaGetLastError();
+  // summaries of a CTA: whole passes, as few as leave about four CTAs an SM
+  const long long groups = (long long)a.B * a.Hkv;
+  long long stretch = ((long long)C * groups + 4 * 148 - 1) / (4 * 148);
+  stretch = (stretch + TS_BLOCKS - 1) / TS_BLOCKS * TS_BLOCKS;
+  e = tree_launch(k_tree_scores<T, S, D>, dim3((unsigned)((C + stretch - 1) / stretch), a.Hkv, a.B),
+                  TS_THREADS, smem, st, a, w, (int)stretch);
   if (e != cudaSuccess) return e;
-  k_tree_select<T, S, D><<<dim3(a.T, a.Hkv, a.B), SEL_THREADS, ksm, st>>>(a, w);
-  return cudaGetLastError();
+  return tree_launch(k_tree_select<T, S, D>, dim3(a.T, a.Hkv, a.B), SEL_THREADS, ksm, st, a, w);
 }
 
 cudaError_t launch_tree_select(const TreeArgs& a, const TreeWs& w, int bf16, int sum_bf16, int d,

@@ -25,6 +25,7 @@ constexpr int TREE_MAX = 64;  // drafted tokens of a sequence: one 64-bit mask a
 struct TreeShared {
   unsigned long long anc[TREE_MAX];  // ancestors of token i, i included
   int up[TREE_MAX];
+  uint32_t early[2];  // tokens whose key lies inside the tail's block
 };
 
 struct TreeSeq {
@@ -34,66 +35,60 @@ struct TreeSeq {
   int tail;   // cached tokens past them
 };
 
-// Lengths of sequence b, clamped to the buffers (a length outside them is
-// reported by the caller that passes err).
-__device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b, uint32_t* err) {
+__device__ __forceinline__ int tree_depth(unsigned long long anc) { return __popcll(anc) - 1; }
+
+// Lengths and ancestor masks of sequence b, by pointer jumping: after round e
+// a token's mask holds its 2^(e+1) nearest ancestors. The three loads go out
+// together. Lengths outside the buffers are clamped, a parent that is not
+// below its child is read as -1; both are reported when err is given. All
+// threads of the block (at least TREE_MAX) call it; it ends with a barrier.
+// No parents: a chain.
+__device__ __forceinline__ TreeSeq tree_load(const TreeArgs& a, int b, TreeShared& t,
+                                             uint32_t* err) {
+  const int i = threadIdx.x;
+  const int n = __ldg(a.lens + b), nt = a.ntok ? __ldg(a.ntok + b) : a.T;
+  int p = i - 1;
+  if (a.parents && i < a.T) p = __ldg(a.parents + (size_t)b * a.T + i);
   TreeSeq s;
-  const int n = a.lens[b], nt = a.ntok ? a.ntok[b] : a.T;
   s.n = min(max(n, 0), a.N);
   s.nt = min(max(nt, 0), a.T);
-  if (err && (s.n != n || s.nt != nt)) atomicOr(err, kErrBadIndex);
   s.c0 = s.n / SAS_BLOCK;
   s.tail = s.n - s.c0 * SAS_BLOCK;
-  return s;
-}
-
-// Ancestor masks by pointer jumping: after round e a token's mask holds its
-// 2^(e+1) nearest ancestors. A parent that is not below its child is reported
-// and read as -1. All threads of the block (at least TREE_MAX) call it; it
-// ends with a barrier. No parents: a chain.
-__device__ __forceinline__ void tree_masks(const TreeArgs& a, int b, int nt, TreeShared& t,
-                                           uint32_t* err) {
-  const int i = threadIdx.x;
-  if (!a.parents) {
-    if (i < TREE_MAX) t.anc[i] = ~0ull >> (63 - i);
-    __syncthreads();
-    return;
-  }
+  if (err && i == 0 && (s.n != n || s.nt != nt)) atomicOr(err, kErrBadIndex);
+  unsigned long long m = 0;
   if (i < TREE_MAX) {
-    int p = -1;
-    if (i < nt) {
-      p = a.parents[(size_t)b * a.T + i];
-      if (p < -1 || p >= i) {
-        if (err) atomicOr(err, kErrBadIndex);
-        p = -1;
-      }
+    if (i >= s.nt) p = -1;
+    if (p < -1 || p >= i) {
+      if (err) atomicOr(err, kErrBadIndex);
+      p = -1;
     }
-    t.anc[i] = 1ull << i;
+    m = a.parents ? 1ull << i : ~0ull >> (63 - i);
+    if (!a.parents) p = -1;
+    t.anc[i] = m;
     t.up[i] = p;
   }
-  __syncthreads();
-#pragma unroll 1
-  for (int e = 0; e < 6; ++e) {
-    unsigned long long m = 0;
-    int p = -1;
-    if (i < TREE_MAX) {
-      m = t.anc[i];
-      p = t.up[i];
-      if (p >= 0) {
-        m |= t.anc[p];
-        p = t.up[p];
-      }
+  while (__syncthreads_or(p >= 0 && i < TREE_MAX)) {  // at most 6 rounds for 64 tokens
+    if (i < TREE_MAX && p >= 0) {
+      m |= t.anc[p];
+      p = t.up[p];
     }
     __syncthreads();
     if (i < TREE_MAX) {
       t.anc[i] = m;
       t.up[i] = p;
     }
-    __syncthreads();
   }
+  if (i < TREE_MAX) {
+    const uint32_t e = __ballot_sync(0xffffffffu, i < s.nt && s.tail + tree_depth(m) < SAS_BLOCK);
+    if ((i & 31) == 0) t.early[i >> 5] = e;
+  }
+  __syncthreads();
+  return s;
 }
 
-__device__ __forceinline__ int tree_depth(unsigned long long anc) { return __popcll(anc) - 1; }
+__device__ __forceinline__ unsigned long long tree_early(const TreeShared& t) {
+  return ((unsigned long long)t.early[1] << 32) | t.early[0];
+}
 
 // Page of logical block m of sequence b (an id outside the pool is reported
 // and replaced by page 0, as in the paged decode).
@@ -147,6 +142,39 @@ struct TreeWs {
   float2* ml;       // [group][split][G T]: running maximum (log2 units) and sum
 };
 
+// The call's kernels overlap by programmatic dependent launch: each one's
+// first part (lengths, tree, queries, tiles of the caller's tensors) runs while
+// the one before it drains; grid_dep_wait() stands before the first access to
+// the workspace. The first kernel waits before anything else and only then
+// lets the next one start, so what the caller's earlier work wrote is complete
+// for all of them. What an earlier kernel of the call wrote is read through L2
+// (__ldcg): a line of it may still lie in an SM's L1.
+template <typename... Params, typename... Args>
+inline cudaError_t tree_launch(void (*kern)(Params...), dim3 grid, int threads, size_t smem,
+                               cudaStream_t st, Args... args) {
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c = {};
+  c.gridDim = grid;
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = st;
+  c.attrs = at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kern, static_cast<Params>(args)...);
+}
+
+// 16 bytes from global to shared memory without a register, zeros when !full.
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool full) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(full ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
 cudaError_t launch_tree_select(const TreeArgs& a, const TreeWs& w, int bf16, int sum_bf16, int d,
                                cudaStream_t st);
 cudaError_t launch_tree_attn_simt(const TreeArgs& a, const TreeWs& w, int d, cudaStream_t st);
@@ -158,21 +186,21 @@ cudaError_t launch_tree_join(const TreeArgs& a, const TreeWs& w, int bf16, int d
 // of the tail's once its path has filled that block.
 __device__ __forceinline__ TreeRow tree_row(const TreeArgs& a, const TreeWs& w, const TreeSeq& s,
                                             size_t group, int i, unsigned long long anc) {
-  if (a.topk > 0) return w.rows[group * a.T + i];
+  if (a.topk > 0) {
+    const float4 x = __ldcg(reinterpret_cast<const float4*>(w.rows + group * a.T + i));
+    TreeRow t;
+    t.lse = x.x;
+    t.th = __float_as_uint(x.y);
+    t.last = __float_as_int(x.z);
+    t.tail_bias = x.w;
+    return t;
+  }
   TreeRow t;
   t.lse = 0.f;
   t.th = 0xffffffffu;
   t.last = -1;
   t.tail_bias = s.tail + tree_depth(anc) >= SAS_BLOCK ? -INFINITY : 0.f;
   return t;
-}
-
-// Drafted tokens whose key lies inside the tail's block.
-__device__ __forceinline__ unsigned long long tree_early(const TreeShared& t, const TreeSeq& s) {
-  unsigned long long m = 0;
-  for (int j = 0; j < s.nt; ++j)
-    if (s.tail + tree_depth(t.anc[j]) < SAS_BLOCK) m |= 1ull << j;
-  return m;
 }
 
 // The units of one split of a (sequence, kv group): the blocks that some
@@ -191,7 +219,7 @@ __device__ __forceinline__ int tree_units(const TreeArgs& a, const uint32_t* __r
     const int lo = min(tid * per, a.words), hi = min(lo + per, a.words);
     int c = 0;
     for (int i = lo; i < hi; ++i) {
-      bits[i] = ubits[i];
+      bits[i] = __ldcg(ubits + i);
       c += __popc(bits[i]);
     }
     int v = c;

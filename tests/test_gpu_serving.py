@@ -479,14 +479,25 @@ def test_decode_tree_ignores_what_a_token_does_not_see(dtype, paged):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-def test_decode_tree_ties_go_to_the_lower_block(dtype):
-    """Equal summaries everywhere: every score ties, the first blocks are kept."""
-    B, Hq, Hkv, d, T, N, topk = 1, 2, 1, 64, 3, 1024, 5
-    x = S.tree_case(4, B, Hq, Hkv, d, T, N, [1000], topk, dtype, "f32", "chain")
-    x["ksum_t"][:] = 0.25
+@pytest.mark.parametrize("N,topk", [(1024, 5), (700 * 64, 33), (1300 * 64, 128)])
+def test_decode_tree_ties_go_to_the_lower_block(dtype, N, topk):
+    """Equal summaries: every score ties and the first blocks are kept; with a
+    better block in the middle, it and the first ones (few and many ties: the
+    list of candidates and the threshold by bits)."""
+    B, Hq, Hkv, d, T = 1, 2, 1, 64, 3
+    q = torch.randn((B, Hq, T, d), generator=torch.Generator().manual_seed(1)).abs() + 0.1
+    q = q.to(S.TORCH[dtype]).to(DEV)
+    kd = torch.zeros((B, Hkv, T, d), dtype=q.dtype, device=DEV)
+    kc = torch.zeros((B, Hkv, N, d), dtype=q.dtype, device=DEV)
+    ks = torch.full((B, Hkv, N // 64, d), 0.25, device=DEV)
     idx = torch.full((B, Hkv, T, topk), -7, dtype=torch.int32, device=DEV)
-    tree_call(x, topk, 1, False, None, idx)
-    assert (idx.cpu() == torch.arange(topk, dtype=torch.int32)).all()
+    o = sas.sas_decode_tree(q, kd, kd, kc, kc, i32([N - 20]), ks, topk, idx_out=idx)
+    assert (idx.cpu() == torch.arange(topk, dtype=torch.int32)).all() and (o == 0).all()
+    mid = N // 64 - 2
+    ks[:, :, mid] = 0.5
+    sas.sas_decode_tree(q, kd, kd, kc, kc, i32([N - 20]), ks, topk, idx_out=idx)
+    want = list(range(topk - 1)) + [mid]
+    assert (idx.cpu() == torch.tensor(want, dtype=torch.int32)).all()
 
 
 def test_decode_tree_of_one_token_is_a_decode_step():
