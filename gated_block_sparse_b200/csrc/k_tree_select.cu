@@ -45,16 +45,27 @@ __device__ __forceinline__ float tf32_hi(float x) {
   return __uint_as_float(__float_as_uint(x) & 0xffffe000u);
 }
 
-// Four consecutive summary elements as fp32.
-__device__ __forceinline__ void load4(const float* p, float (&x)[4]) {
-  const float4 v = __ldg(reinterpret_cast<const float4*>(p));
-  x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-}
-__device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&x)[4]) {
-  const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-  x[0] = __uint_as_float(v.x << 16); x[1] = __uint_as_float(v.x & 0xffff0000u);
-  x[2] = __uint_as_float(v.y << 16); x[3] = __uint_as_float(v.y & 0xffff0000u);
-}
+// Four consecutive summary elements as loaded.
+template <typename S> struct Raw;
+template <> struct Raw<float> {
+  float4 v;
+  __device__ __forceinline__ void load(const float* p) {
+    v = __ldg(reinterpret_cast<const float4*>(p));
+  }
+  __device__ __forceinline__ float get(int i) const {
+    return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+  }
+};
+template <> struct Raw<__nv_bfloat16> {
+  uint2 v;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    v = __ldg(reinterpret_cast<const uint2*>(p));
+  }
+  __device__ __forceinline__ float get(int i) const {
+    const uint32_t w = i < 2 ? v.x : v.y;
+    return __uint_as_float((i & 1) ? (w & 0xffff0000u) : (w << 16));
+  }
+};
 
 }  // namespace
 
@@ -65,7 +76,7 @@ __device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&x)[4]) {
 // 4c .. 4c + 3, one 16-byte load, as k = c and c + 4 of two steps. Rows of
 // shared memory are D + 16 floats apart, so that those loads meet no bank twice.
 template <typename T, typename S, int D>
-__global__ void __launch_bounds__(TS_THREADS) k_tree_scores(TreeArgs a, TreeWs w, int stretch) {
+__global__ void __launch_bounds__(TS_THREADS, 3) k_tree_scores(TreeArgs a, TreeWs w, int stretch) {
   constexpr int LD = D + 16, VT = Vec16<T>::N, KG = D / 16;
   constexpr bool SPLIT = sizeof(S) == 4;
   extern __shared__ __align__(16) float sm_f[];
@@ -84,48 +95,61 @@ __global__ void __launch_bounds__(TS_THREADS) k_tree_scores(TreeArgs a, TreeWs w
   const int c0 = min(max(n, 0), a.N) / SAS_BLOCK, nt = min(max(ntk, 0), a.T);
   const int m_hi = min(m_lo + stretch, c0);
   if (m_lo >= m_hi || nt == 0) return;
-  const float inv_g = 1.0f / (float)G;
-  for (int e = tid; e < T8 * (D / VT); e += TS_THREADS) {
-    const int row = e / (D / VT), c = (e % (D / VT)) * VT;
-    float x[VT];
+  // A of a pass: rows quad and quad + 8 of the warp's 16 (a row past the end
+  // reads the last one), loaded a pass ahead
+  const int quad = lane >> 2, c = lane & 3, ntiles = (nt + 7) >> 3;
+  const S* sums = static_cast<const S*>(a.ksum) + 4 * c;
+  auto row_at = [&](int m) -> size_t {
+    m = min(m, m_hi - 1);
+    return (a.table ? (size_t)tree_page(a, b, m, &g_tree_select_err) * a.Hkv + r : group * C + m) * D;
+  };
+  Raw<S> x[2][KG];
+  size_t at[2];
+  int m0 = m_lo + wid * 16;
 #pragma unroll
-    for (int i = 0; i < VT; ++i) x[i] = 0.f;
+  for (int h = 0; h < 2; ++h) {
+    at[h] = row_at(m0 + quad + 8 * h);
+#pragma unroll
+    for (int g = 0; g < KG; ++g) x[h][g].load(sums + at[h] + 16 * g);
+    at[h] = row_at(m0 + TS_BLOCKS + quad + 8 * h);
+  }
+  const float inv_g = 1.0f / (float)G;
+#pragma unroll 2
+  for (int e = tid; e < T8 * (D / VT); e += TS_THREADS) {
+    const int row = e / (D / VT), col = (e % (D / VT)) * VT;
+    float s[VT];
+#pragma unroll
+    for (int i = 0; i < VT; ++i) s[i] = 0.f;
     if (row < nt) {
-      const T* q = static_cast<const T*>(a.q) + (((size_t)b * a.Hq + r * G) * a.T + row) * D + c;
+      const T* q = static_cast<const T*>(a.q) + (((size_t)b * a.Hq + r * G) * a.T + row) * D + col;
 #pragma unroll 4
       for (int g = 0; g < G; ++g) {
         float y[VT];
         Vec16<T>::load_nc(q + (size_t)g * a.T * D, y);
 #pragma unroll
-        for (int i = 0; i < VT; ++i) x[i] += y[i];
+        for (int i = 0; i < VT; ++i) s[i] += y[i];
       }
     }
 #pragma unroll
-    for (int i = 0; i < VT; ++i) {
-      const float m = x[i] * inv_g, h = tf32_hi(m);
-      qh[row * LD + c + i] = h;
-      ql[row * LD + c + i] = tf32_hi(m - h);
+    for (int i = 0; i < VT; i += 4) {
+      float4 h, l;
+      const float m[4] = {s[i] * inv_g, s[i + 1] * inv_g, s[i + 2] * inv_g, s[i + 3] * inv_g};
+      h = make_float4(tf32_hi(m[0]), tf32_hi(m[1]), tf32_hi(m[2]), tf32_hi(m[3]));
+      l = make_float4(tf32_hi(m[0] - h.x), tf32_hi(m[1] - h.y), tf32_hi(m[2] - h.z),
+                      tf32_hi(m[3] - h.w));
+      *reinterpret_cast<float4*>(qh + row * LD + col + i) = h;
+      *reinterpret_cast<float4*>(ql + row * LD + col + i) = l;
     }
   }
   __syncthreads();
-  const int quad = lane >> 2, c = lane & 3, ntiles = (nt + 7) >> 3;
-  for (int m0 = m_lo + wid * 16; m0 < m_hi; m0 += TS_BLOCKS) {
-    // A: rows quad and quad + 8 of the warp's 16 (a row past the end reads the last one)
-    float x[2][KG][4];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int m = min(m0 + quad + 8 * h, m_hi - 1);
-      const size_t at =
-          a.table ? (size_t)tree_page(a, b, m, &g_tree_select_err) * a.Hkv + r : group * C + m;
-      const S* p = static_cast<const S*>(a.ksum) + at * D + 4 * c;
-#pragma unroll
-      for (int g = 0; g < KG; ++g) load4(p + 16 * g, x[h][g]);
-    }
+  float* out = w.scores + group * a.T * C;
+  for (; m0 < m_hi; m0 += TS_BLOCKS) {
     float acc[TREE_MAX / 8][4];
 #pragma unroll
     for (int j = 0; j < TREE_MAX / 8; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
+    const bool more = m0 + TS_BLOCKS < m_hi;
 #pragma unroll
     for (int g = 0; g < KG; ++g) {
       float hi[2][4], lo[2][4];  // of the two k steps of this group
@@ -133,35 +157,54 @@ __global__ void __launch_bounds__(TS_THREADS) k_tree_scores(TreeArgs a, TreeWs w
       for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {  // fragment i: row half i & 1, k half i >> 1
-          const float v = x[i & 1][g][2 * k + (i >> 1)];
+          const float v = x[i & 1][g].get(2 * k + (i >> 1));
           hi[k][i] = SPLIT ? tf32_hi(v) : v;
           lo[k][i] = SPLIT ? tf32_hi(v - hi[k][i]) : 0.f;
         }
+      if (more) {  // this group's registers take the next pass's values
 #pragma unroll
-      for (int j = 0; j < TREE_MAX / 8; ++j) {
-        if (j < ntiles) {
-          const int at = (8 * j + quad) * LD + 16 * g + 4 * c;
-          const float4 bh = *reinterpret_cast<const float4*>(qh + at);
-          const float4 bl = *reinterpret_cast<const float4*>(ql + at);
-          mma_tf32(acc[j], hi[0], bl.x, bl.y);
-          mma_tf32(acc[j], hi[1], bl.z, bl.w);
-          if (SPLIT) {
-            mma_tf32(acc[j], lo[0], bh.x, bh.y);
-            mma_tf32(acc[j], lo[1], bh.z, bh.w);
+        for (int h = 0; h < 2; ++h) x[h][g].load(sums + at[h] + 16 * g);
+      }
+      // four token tiles at a time: consecutive MMAs go to different sums
+#pragma unroll
+      for (int j0 = 0; j0 < TREE_MAX / 8; j0 += 4) {
+        if (j0 >= ntiles) break;
+        float4 bh[4], bl[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (j0 + j < ntiles) {
+            const int o = (8 * (j0 + j) + quad) * LD + 16 * g + 4 * c;
+            bh[j] = *reinterpret_cast<const float4*>(qh + o);
+            bl[j] = *reinterpret_cast<const float4*>(ql + o);
           }
-          mma_tf32(acc[j], hi[0], bh.x, bh.y);
-          mma_tf32(acc[j], hi[1], bh.z, bh.w);
+#define SAS_EACH(A, X, Y)              \
+  _Pragma("unroll") for (int j = 0; j < 4; ++j) if (j0 + j < ntiles) \
+      mma_tf32(acc[j0 + j], A, X, Y)
+        SAS_EACH(hi[0], bl[j].x, bl[j].y);
+        SAS_EACH(hi[1], bl[j].z, bl[j].w);
+        if (SPLIT) {
+          SAS_EACH(lo[0], bh[j].x, bh[j].y);
+          SAS_EACH(lo[1], bh[j].z, bh[j].w);
         }
+        SAS_EACH(hi[0], bh[j].x, bh[j].y);
+        SAS_EACH(hi[1], bh[j].z, bh[j].w);
+#undef SAS_EACH
       }
     }
+    if (more) {
 #pragma unroll
-    for (int j = 0; j < TREE_MAX / 8; ++j)
+      for (int h = 0; h < 2; ++h) at[h] = row_at(m0 + 2 * TS_BLOCKS + quad + 8 * h);
+    }
+    float* o = out + (size_t)(2 * c) * C + m0 + quad;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {  // row quad + 8 (i >> 1), column 2 c + (i & 1)
-        const int t = 8 * j + 2 * c + (i & 1), m = m0 + quad + 8 * (i >> 1);
-        if (t < nt && m < m_hi)
-          w.scores[(group * a.T + t) * C + m] = acc[j][i] * a.scale + 0.f;
+    for (int j = 0; j < TREE_MAX / 8; ++j) {
+      if (j < ntiles) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)  // row quad + 8 (i >> 1), column 2 c + (i & 1)
+          if (8 * j + 2 * c + (i & 1) < nt && m0 + quad + 8 * (i >> 1) < m_hi)
+            o[(size_t)(8 * j + (i & 1)) * C + 8 * (i >> 1)] = acc[j][i] * a.scale + 0.f;
       }
+    }
   }
 }
 
@@ -408,9 +451,13 @@ static cudaError_t launch_typed(const TreeArgs& a, const TreeWs& w, cudaStream_t
   const size_t ksm = (size_t)(C + 1) * sizeof(uint32_t);
   e = ensure_smem(k_tree_select<T, S, D>, ksm);
   if (e != cudaSuccess) return e;
-  // summaries of a CTA: whole passes, as few as leave about four CTAs an SM
+  // summaries of a CTA: whole passes, and one wave of the CTAs that an SM holds
+  // (three by registers, fewer by shared memory)
   const long long groups = (long long)a.B * a.Hkv;
-  long long stretch = ((long long)C * groups + 4 * 148 - 1) / (4 * 148);
+  const long long room = 148 * (smem > 75 * 1024 ? 2 : 3);
+  long long per_group = room / groups;
+  if (per_group < 1) per_group = 1;
+  long long stretch = (C + per_group - 1) / per_group;
   stretch = (stretch + TS_BLOCKS - 1) / TS_BLOCKS * TS_BLOCKS;
   e = tree_launch(k_tree_scores<T, S, D>, dim3((unsigned)((C + stretch - 1) / stretch), a.Hkv, a.B),
                   TS_THREADS, smem, st, a, w, (int)stretch);
