@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(TA_THREADS) k_tree_attn_simt(TreeArgs a, TreeW
       float bias[2] = {-INFINITY, -INFINITY};
       if (row < rows) {
         if (u < nu) {
-          const float sc = __ldcg(w.scores + (group * a.T + tok[i]) * (a.N / SAS_BLOCK) + blk);
+          const float sc = __ldcg(w.scores + (group * a.T + tok[i]) * tree_stride(a.N / SAS_BLOCK) + blk);
           bias[0] = bias[1] = tree_bias(info[i], sc, blk, a.gated) * LOG2E;
         } else {
 #pragma unroll
@@ -172,71 +172,72 @@ __global__ void __launch_bounds__(TA_THREADS) k_tree_attn_simt(TreeArgs a, TreeW
     const size_t at = (group * a.ns + split) * (size_t)(G * a.T) + row;
     if (lane == 0) w.ml[at] = make_float2(m[i], l[i]);
     if (l[i] != 0.f) {
-#pragma unroll
-      for (int e = 0; e < E; ++e) w.part[at * D + lane * E + e] = acc[i][e];
+      float* out = w.part + ((group * a.ns + split) * (size_t)(G * a.T)) * D + (size_t)row * 4 +
+                   tree_part_at(lane * E, (size_t)G * a.T);
+      if constexpr (E == 4)
+        *reinterpret_cast<float4*>(out) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+      else
+        *reinterpret_cast<float2*>(out) = make_float2(acc[i][0], acc[i][1]);
     }
   }
 }
 
-// Joins the splits: o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s, one
-// warp per row, lane s holding split s's maximum and sum (at most 32 splits).
-// A split that saw none of a row's keys has l = 0, and its partial output is
-// not read. Latency bounds it: the partial outputs are loaded eight at a time.
+// Joins the splits: o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s. One CTA
+// per 8 rows: warp w first turns row w's maxima and sums into one factor per
+// split (lane s; at most 32 splits), then thread (row, four columns) adds the
+// partial outputs, eight splits in flight. A split that saw none of a row's
+// keys has l = 0, and its partial output is not read. Eight rows side by side
+// make every access a full 32-byte sector. Latency bounds it.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) k_tree_join(TreeArgs a, TreeWs w) {
-  constexpr int E = D / 32;
-  const int b = blockIdx.z, r = blockIdx.y, lane = threadIdx.x & 31;
-  const int G = a.Hq / a.Hkv, row = blockIdx.x * 8 + (threadIdx.x >> 5);
+  constexpr int ROWS = 8, PER = D / 4;
+  __shared__ float fs[ROWS][32];
+  const int b = blockIdx.z, r = blockIdx.y, lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int G = a.Hq / a.Hkv, row0 = blockIdx.x * ROWS;
   const int nt = min(max(a.ntok ? __ldg(a.ntok + b) : a.T, 0), a.T);
   grid_dep_wait();
-  if (row >= G * nt) return;
+  const int rows = G * nt;
+  if (row0 >= rows) return;
   const size_t group = (size_t)b * a.Hkv + r, R = (size_t)G * a.T;
-  const size_t at0 = group * a.ns * R + row;
   float2 ml = make_float2(-1e30f, 0.f);
-  if (lane < a.ns) ml = __ldcg(w.ml + at0 + lane * R);
+  if (lane < a.ns && row0 + wid < rows)
+    ml = __ldcg(w.ml + (group * a.ns + lane) * R + row0 + wid);
   const bool seen = ml.y != 0.f;
   const float M = warp_max(seen ? ml.x : -INFINITY);
   const float f = seen ? exp2f(ml.x - M) : 0.f;
   const float L = warp_sum(seen ? ml.y * f : 0.f);
-  const unsigned live = __ballot_sync(0xffffffffu, seen);
-  float acc[E];
+  fs[wid][lane] = seen ? f / L : -1.f;  // -1: not read
+  __syncthreads();
+  const int i = threadIdx.x % ROWS, c4 = threadIdx.x / ROWS, row = row0 + i;
+  if (c4 >= PER || row >= rows) return;
+  const float* src = w.part + group * a.ns * R * D + ((size_t)c4 * R + row) * 4;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = 0; s0 < a.ns; s0 += 8) {
+    float4 x[8];
+    float g[8];
 #pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  const float* src = w.part + at0 * D + lane * E;
-  for (int i0 = 0; i0 < a.ns; i0 += 8) {
-    float x[8][E];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-#pragma unroll
-      for (int e = 0; e < E; ++e) x[i][e] = 0.f;
-      if (live >> (i0 + i) & 1u) {
-        const float* p = src + (size_t)(i0 + i) * R * D;
-        if constexpr (E == 4) {
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(p));
-          x[i][0] = v.x; x[i][1] = v.y; x[i][2] = v.z; x[i][3] = v.w;
-        } else {
-          const float2 v = __ldcg(reinterpret_cast<const float2*>(p));
-          x[i][0] = v.x; x[i][1] = v.y;
-        }
-      }
+    for (int k = 0; k < 8; ++k) {
+      g[k] = s0 + k < a.ns ? fs[i][s0 + k] : -1.f;
+      x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (!(g[k] < 0.f)) x[k] = __ldcg(reinterpret_cast<const float4*>(src + (s0 + k) * R * D));
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float fi = __shfl_sync(0xffffffffu, f, i0 + i);
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = fmaf(x[i][e], fi, acc[e]);
+    for (int k = 0; k < 8; ++k) {
+      acc.x = fmaf(x[k].x, g[k], acc.x);
+      acc.y = fmaf(x[k].y, g[k], acc.y);
+      acc.z = fmaf(x[k].z, g[k], acc.z);
+      acc.w = fmaf(x[k].w, g[k], acc.w);
     }
   }
   T* o = static_cast<T*>(a.o) +
-         (((size_t)b * a.Hq + r * G + row / nt) * a.T + row % nt) * D + lane * E;
-  const float inv = 1.0f / L;
-#pragma unroll
-  for (int e = 0; e < E; e += 2) {
-    if constexpr (sizeof(T) == 2)
-      *reinterpret_cast<__nv_bfloat162*>(o + e) =
-          __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
-    else
-      *reinterpret_cast<float2*>(o + e) = make_float2(acc[e] * inv, acc[e + 1] * inv);
+         (((size_t)b * a.Hq + r * G + row / nt) * a.T + row % nt) * D + c4 * 4;
+  if constexpr (sizeof(T) == 2) {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y);
+    const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z, acc.w);
+    *reinterpret_cast<uint2*>(o) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                                              *reinterpret_cast<const uint32_t*>(&hi));
+  } else {
+    *reinterpret_cast<float4*>(o) = acc;
   }
 }
 

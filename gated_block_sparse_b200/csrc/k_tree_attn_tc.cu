@@ -66,6 +66,38 @@ __device__ __forceinline__ void mma_tmem_a(uint32_t tmem_d, uint32_t tmem_a, uin
       : "memory");
 }
 
+// (a0, a1) = (x0, x1) * c + (o, o) as one packed fp32x2 FMA
+__device__ __forceinline__ void fma2c(float& a0, float& a1, float x0, float x1, float c, float o) {
+  asm("{\n\t.reg .b64 x, c, o, a;\n\t"
+      "mov.b64 x, {%2, %3};\n\t"
+      "mov.b64 c, {%4, %4};\n\t"
+      "mov.b64 o, {%5, %5};\n\t"
+      "fma.rn.f32x2 a, x, c, o;\n\t"
+      "mov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(a0), "=f"(a1)
+      : "f"(x0), "f"(x1), "f"(c), "f"(o));
+}
+// (s0, s1) += (x0, x1) as one packed fp32x2 add
+__device__ __forceinline__ void add2(float& s0, float& s1, float x0, float x1) {
+  asm("{\n\t.reg .b64 s, x;\n\t"
+      "mov.b64 s, {%0, %1};\n\t"
+      "mov.b64 x, {%2, %3};\n\t"
+      "add.rn.f32x2 s, s, x;\n\t"
+      "mov.b64 {%0, %1}, s;\n\t}"
+      : "+f"(s0), "+f"(s1)
+      : "f"(x0), "f"(x1));
+}
+// max(a, b, c) in one instruction
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// Barrier 1 over the softmax and MMA warps (the TMA warp is not in it).
+__device__ __forceinline__ void sync_but_tma() {
+  asm volatile("bar.sync 1, %0;" ::"n"(TT_THREADS - 32) : "memory");
+}
+
 // Offset of 16-byte piece p of row `row` in a K-major tile of `nrows` rows
 // under the 128-byte swizzle: 64-column chunks one after the other, rows of
 // 128 bytes, the piece's index within the row xor (row mod 8).
@@ -88,9 +120,9 @@ __device__ __noinline__ float2 repair_row(const TreeArgs& a, const TreeWs& w, co
                                           int start, float* out) {
   const __nv_bfloat16* kc = static_cast<const __nv_bfloat16*>(a.kc);
   const __nv_bfloat16* vc = static_cast<const __nv_bfloat16*>(a.vc);
-  const size_t group = (size_t)b * a.Hkv + r;
+  const size_t group = (size_t)b * a.Hkv + r, R = (size_t)(a.Hq / a.Hkv) * a.T;
   float m = -1e30f, l = 0.f;
-  for (int c = 0; c < D; ++c) out[c] = 0.f;
+  for (int c = 0; c < D; ++c) out[tree_part_at(c, R)] = 0.f;
   for (int pass = 0; pass < 2; ++pass) {  // the maximum first, then the sums
     int blk = -1;
     for (int u = u0; u < u1; ++u) {
@@ -100,7 +132,7 @@ __device__ __noinline__ float2 repair_row(const TreeArgs& a, const TreeWs& w, co
       if (u <= nu) {
         if (u < nu) {
           blk = u == u0 ? start : tree_next(bits, a.words, blk + 1);
-          bias = tree_bias(rs.info, __ldcg(w.scores + (group * a.T + rs.tok) * (a.N / SAS_BLOCK) + blk),
+          bias = tree_bias(rs.info, __ldcg(w.scores + (group * a.T + rs.tok) * tree_stride(a.N / SAS_BLOCK) + blk),
                            blk, a.gated);
         } else {
           nk = s.tail;
@@ -130,7 +162,10 @@ __device__ __noinline__ float2 repair_row(const TreeArgs& a, const TreeWs& w, co
           const float p = exp2f(z - m);
           l += p;
           if (p != 0.f)
-            for (int c = 0; c < D; ++c) out[c] = fmaf(p, to_f(vp[(size_t)j * D + c]), out[c]);
+            for (int c = 0; c < D; ++c) {
+              float& x = out[tree_part_at(c, R)];
+              x = fmaf(p, to_f(vp[(size_t)j * D + c]), x);
+            }
         }
       }
     }
@@ -180,10 +215,15 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
     fence_mbar_init();
   }
   if (warp == 5) tc::tmem_alloc(tmem_slot, 256);
+  if (tid == 128) {
+    tc::prefetch_map(&kmap);
+    tc::prefetch_map(&vmap);
+  }
   // Q: rows of the group's heads, zeros behind the last (only as far as the
   // softmax warps look; other rows' products are never read)
   const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
-  for (int e = tid; e < nwarp * 32 * PC; e += TT_THREADS) {
+  for (int e = warp == 5 ? 128 + lane : tid; warp != 4 && e < nwarp * 32 * PC;
+       e += TT_THREADS - 32) {
     const int row = e / PC, p = e % PC, gr = min(row0 + row, rows - 1);
     cp_async16(sm + L::Q + sw_off(row, p, 128),
                q + (((size_t)b * a.Hq + r * G + gr / s.nt) * a.T + gr % s.nt) * D + p * 8,
@@ -198,58 +238,18 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
   const bool has_draft = u0 <= nu + 1 && nu + 1 < u1;
   const int nsp = (int)has_tail + (int)has_draft;
   const int nh = max(0, min(u1, nu) - u0), nunits = nsp + nh;
-  const size_t prow = (group * a.ns + split) * (size_t)(G * a.T) + row0 + tid;
-  // the units that end inside a tile
-  for (int j = 0; j < nsp; ++j) {
-    const bool is_tail = has_tail && j == 0;
-    const int nk = is_tail ? s.tail : s.nt;
-    const __nv_bfloat16 *kp, *vp;
-    if (is_tail) {
-      const size_t at = tree_block_row(a, b, r, s.c0, err) * D;
-      kp = static_cast<const __nv_bfloat16*>(a.kc) + at;
-      vp = static_cast<const __nv_bfloat16*>(a.vc) + at;
-    } else {
-      kp = static_cast<const __nv_bfloat16*>(a.kd) + group * a.T * D;
-      vp = static_cast<const __nv_bfloat16*>(a.vd) + group * a.T * D;
-    }
-    unsigned char* st = sm + L::KV + j * 2 * L::TILE;
-#pragma unroll 2
-    for (int e = tid; e < 64 * PC; e += TT_THREADS) {
-      const int row = e / PC, p = e % PC, from = min(row, nk - 1);
-      cp_async16(st + sw_off(row, p, 64), kp + (size_t)from * D + p * 8, row < nk);
-      cp_async16(st + L::TILE + sw_off(row, p, 64), vp + (size_t)from * D + p * 8, row < nk);
-    }
-  }
-  cp_async_wait();
-  fence_proxy_async_smem();  // the tiles above are read by the tensor cores
-  tc::fence_before_sync();
-  __syncthreads();
-  tc::fence_after_sync();
-  const uint32_t tmem = *tmem_slot;
-  if (nunits == 0) {  // more splits than units
-    if (tid < 128 && row0 + tid < rows) w.ml[prow] = make_float2(-1e30f, 0.f);
-    if (warp == 5) tc::tmem_dealloc(tmem, 256);
-    return;
-  }
-  const uint32_t tm_s[2] = {tmem, tmem + 64};
-  const uint32_t tm_o = tmem + 128;
+  const size_t R = (size_t)G * a.T, prow = (group * a.ns + split) * R + row0 + tid;
   const int start = nh > 0 ? start_s : 0;
-
   if (warp == 4) {
     // ---------------------------------------------------------------- producer
     if (lane < 2) {
       const bool kl = lane == 0;
       const CUtensorMap* map = kl ? &kmap : &vmap;
-      tc::prefetch_map(map);
       uint64_t* fullb = &bars[kl ? B_KF : B_VF];
       uint64_t* emptyb = &bars[kl ? B_KE : B_VE];
       int blk = start - 1;
-      for (int j = 0; j < nunits; ++j) {
+      for (int j = nsp; j < nunits; ++j) {
         const int st = j & 1;
-        if (j < nsp) {
-          mbar_arrive(&fullb[st]);  // written above
-          continue;
-        }
         if (j >= 2) mbar_wait_data(&emptyb[st], ((j >> 1) - 1) & 1, err);
         blk = tree_next(bits, a.words, blk + 1);
         int y = 64 * blk, z = (int)group;
@@ -264,12 +264,50 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
           tc::tma_load_3d(dst + c * 8192, map, 64 * c, y, z, &fullb[st]);
       }
     }
+  } else {
+    // the units that end inside a tile
+    const int t = warp == 5 ? 128 + lane : tid;
+    for (int j = 0; j < nsp; ++j) {
+      const bool is_tail = has_tail && j == 0;
+      const int nk = is_tail ? s.tail : s.nt;
+      const __nv_bfloat16 *kp, *vp;
+      if (is_tail) {
+        const size_t at = tree_block_row(a, b, r, s.c0, err) * D;
+        kp = static_cast<const __nv_bfloat16*>(a.kc) + at;
+        vp = static_cast<const __nv_bfloat16*>(a.vc) + at;
+      } else {
+        kp = static_cast<const __nv_bfloat16*>(a.kd) + group * a.T * D;
+        vp = static_cast<const __nv_bfloat16*>(a.vd) + group * a.T * D;
+      }
+      unsigned char* st = sm + L::KV + j * 2 * L::TILE;
+#pragma unroll 2
+      for (int e = t; e < 64 * PC; e += TT_THREADS - 32) {
+        const int row = e / PC, p = e % PC, from = min(row, nk - 1);
+        cp_async16(st + sw_off(row, p, 64), kp + (size_t)from * D + p * 8, row < nk);
+        cp_async16(st + L::TILE + sw_off(row, p, 64), vp + (size_t)from * D + p * 8, row < nk);
+      }
+    }
+    cp_async_wait();
+    fence_proxy_async_smem();  // the tiles above are read by the tensor cores
+    tc::fence_before_sync();
+    sync_but_tma();
+    tc::fence_after_sync();
+  }
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t tm_s[2] = {tmem, tmem + 64};
+  const uint32_t tm_o = tmem + 128;
+  if (nunits == 0) {  // more splits than units
+    if (tid < 128 && row0 + tid < rows) w.ml[prow] = make_float2(-1e30f, 0.f);
   } else if (warp == 5) {
     // ---------------------------------------------------------------- MMA issuer
     if (lane == 0) {
       constexpr uint32_t ID_QK = tc::idesc_bf16(128, 64, 0, 0);
       constexpr uint32_t ID_PV = tc::idesc_bf16(128, D, 0, 1);
       const uint32_t q_addr = smem_u32(sm + L::Q);
+      for (int j = 0; j < nsp; ++j) {  // written above
+        mbar_arrive(&bars[B_KF + j]);
+        mbar_arrive(&bars[B_VF + j]);
+      }
       auto pv = [&](int j) {  // O += P_j V_j
         mbar_wait(&bars[B_PF], j & 1, err);
         mbar_wait_data(&bars[B_VF + (j & 1)], (j >> 1) & 1, err);
@@ -314,7 +352,7 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
     rs.anc = tree.anc[rs.tok];
     rs.early = tree_early(tree);
     rs.info = tree_row(a, w, s, group, rs.tok, rs.anc);
-    const float* sc = w.scores + (group * a.T + rs.tok) * (size_t)(a.N / SAS_BLOCK);
+    const float* sc = w.scores + (group * a.T + rs.tok) * tree_stride(a.N / SAS_BLOCK);
     float m = -1e30f, l = 0.f;
     int blk = start - 1;
     float next_score = 0.f;
@@ -367,11 +405,11 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
       }
       float zm[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) zm[c] = z[c];
+      for (int c = 0; c < 4; ++c) zm[c] = fmaxf(z[2 * c], z[2 * c + 1]);
 #pragma unroll
-      for (int i = 4; i < 64; i += 4) {
+      for (int i = 8; i < 64; i += 8) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) zm[c] = fmaxf(zm[c], z[i + c]);
+        for (int c = 0; c < 4; ++c) zm[c] = max3(zm[c], z[i + 2 * c], z[i + 2 * c + 1]);
       }
       // c1 > 0, so the maximum of z c1 + bias is that of z
       const float mx =
@@ -380,16 +418,22 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
       const bool grow = (j == 0) || (mnew > m + RESCALE_LOG2);
       const float muse = grow ? mnew : m;
       const float off = bias - muse;
-      float rsum = 0.f;
+      float r0 = 0.f, r1 = 0.f;
       uint32_t pk[32];
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
-        float p0 = tc::ex2(fmaf(z[2 * i], c1, off)), p1 = tc::ex2(fmaf(z[2 * i + 1], c1, off));
-        p0 = dead ? 0.f : p0;
-        p1 = dead ? 0.f : p1;
-        rsum += p0 + p1;
+        float a0, a1;
+        fma2c(a0, a1, z[2 * i], z[2 * i + 1], c1, off);
+        const float p0 = tc::ex2(a0), p1 = tc::ex2(a1);
+        add2(r0, r1, p0, p1);
         __nv_bfloat162 h2 = __floats2bfloat162_rn(p0, p1);
         pk[i] = *reinterpret_cast<uint32_t*>(&h2);
+      }
+      float rsum = r0 + r1;
+      if (dead) {  // whatever the products were, NaN included
+        rsum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) pk[i] = 0u;
       }
       if (j > 0) {
         // PV_{j-1} done before O is rescaled. Waiting on every unit also keeps
@@ -429,7 +473,7 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
     // epilogue: the split's sums, and O before the division
     mbar_wait_data(&bars[B_OD], (nunits - 1) & 1, err);
     tc::fence_after_sync();
-    float* out = w.part + prow * D;
+    float* out = w.part + (group * a.ns + split) * R * D + (size_t)row * 4;
     bool bad = !(fabsf(l) < INFINITY);
 #pragma unroll 1
     for (int c = 0; c < D / 32; ++c) {
@@ -441,7 +485,7 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
         for (int i = 0; i < 32; ++i) bad |= !(fabsf(ov[i]) < INFINITY);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          *reinterpret_cast<float4*>(out + 32 * c + 4 * i) =
+          *reinterpret_cast<float4*>(out + tree_part_at(32 * c + 4 * i, R)) =
               make_float4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
       }
     }

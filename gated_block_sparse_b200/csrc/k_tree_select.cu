@@ -142,7 +142,8 @@ __global__ void __launch_bounds__(TS_THREADS, 3) k_tree_scores(TreeArgs a, TreeW
     }
   }
   __syncthreads();
-  float* out = w.scores + group * a.T * C;
+  const int CS = tree_stride(C);
+  float* out = w.scores + group * a.T * CS;
   for (; m0 < m_hi; m0 += TS_BLOCKS) {
     float acc[TREE_MAX / 8][4];
 #pragma unroll
@@ -195,14 +196,14 @@ __global__ void __launch_bounds__(TS_THREADS, 3) k_tree_scores(TreeArgs a, TreeW
 #pragma unroll
       for (int h = 0; h < 2; ++h) at[h] = row_at(m0 + 2 * TS_BLOCKS + quad + 8 * h);
     }
-    float* o = out + (size_t)(2 * c) * C + m0 + quad;
+    float* o = out + (size_t)(2 * c) * CS + m0 + quad;
 #pragma unroll
     for (int j = 0; j < TREE_MAX / 8; ++j) {
       if (j < ntiles) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)  // row quad + 8 (i >> 1), column 2 c + (i & 1)
           if (8 * j + 2 * c + (i & 1) < nt && m0 + quad + 8 * (i >> 1) < m_hi)
-            o[(size_t)(8 * j + (i & 1)) * C + 8 * (i >> 1)] = acc[j][i] * a.scale + 0.f;
+            o[(size_t)(8 * j + (i & 1)) * CS + 8 * (i >> 1)] = acc[j][i] * a.scale + 0.f;
       }
     }
   }
@@ -212,6 +213,7 @@ namespace {
 constexpr int SEL_THREADS = 256;
 constexpr int SEL_WARPS = SEL_THREADS / 32;
 constexpr int SEL_LIST = 512;  // candidates ranked by counting
+constexpr float LOG2E = 1.4426950408889634f;
 }  // namespace
 
 __device__ __forceinline__ float block_sum(float v, float* red) {
@@ -275,7 +277,7 @@ __device__ __noinline__ void select_by_bits(const uint32_t* keys, int lo, int hi
 
 template <typename T, typename S, int D>
 __global__ void __launch_bounds__(SEL_THREADS) k_tree_select(TreeArgs a, TreeWs w) {
-  extern __shared__ __align__(16) uint32_t keys[];  // C_i keys
+  extern __shared__ __align__(16) float vals[];  // C_i scores
   __shared__ TreeShared tree;
   __shared__ float red[SEL_WARPS];
   __shared__ uint32_t scan[SEL_WARPS];
@@ -339,22 +341,29 @@ __global__ void __launch_bounds__(SEL_THREADS) k_tree_select(TreeArgs a, TreeWs 
     th_s = 0xffffffffu;
   }
   grid_dep_wait();
-  const float* sc = w.scores + row * C;
+  // Scores: four at a time into shared memory, with the thread's maximum; the
+  // tail's block last.
+  const float* sc = w.scores + row * tree_stride(C);
   float mx = -INFINITY;
-  uint32_t best = 0;  // below every key of a finite score
-#pragma unroll 8
-  for (int m = tid; m < Ci; m += SEL_THREADS) {
-    const float v = m < s.c0 ? __ldcg(sc + m) : virt;
-    const uint32_t key = score_key(v);
-    keys[m] = key;
-    best = max(best, key);
-    mx = fmaxf(mx, v);
+#pragma unroll 4
+  for (int m = 4 * tid; m < s.c0; m += 4 * SEL_THREADS) {
+    float4 v = __ldcg(reinterpret_cast<const float4*>(sc + m));
+    if (m + 1 >= s.c0) v.y = -INFINITY;
+    if (m + 2 >= s.c0) v.z = -INFINITY;
+    if (m + 3 >= s.c0) v.w = -INFINITY;
+    *reinterpret_cast<float4*>(vals + m) = v;
+    mx = fmaxf(mx, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
   }
+  const uint32_t best = mx > -INFINITY ? score_key(mx) : 0u;  // a subset's keys bound the set's
   mx = warp_max(mx);
   if (lane == 0) red[wid] = mx;
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < SEL_WARPS; ++k) mx = fmaxf(mx, red[k]);
+  if (crossed) {
+    mx = fmaxf(mx, virt);
+    if (tid == 0) vals[s.c0] = virt;
+  }
   // A lower bound of the kk-th best key: that of the threads' own best ones (a
   // subset), by its upper 16 bits.
   uint32_t bound = 0;
@@ -363,19 +372,33 @@ __global__ void __launch_bounds__(SEL_THREADS) k_tree_select(TreeArgs a, TreeWs 
     const uint32_t cand = bound | (1u << bit);
     if (__syncthreads_count(best >= cand) >= kk) bound = cand;
   }
+  // The sum of the gate's softmax, and the list of the keys at or above the bound.
   float sum = 0.f;
-  for (int m0 = 0; m0 < Ci; m0 += SEL_THREADS) {
-    const int m = m0 + tid;
-    const uint32_t key = m < Ci ? keys[m] : 0u;
-    if (m < Ci) sum += expf(score_of(key) - mx);
-    const bool keep = m < Ci && key >= bound;
-    const unsigned mask = __ballot_sync(0xffffffffu, keep);
-    if (mask) {
-      int base = 0;
-      if (lane == 0) base = atomicAdd(&cnt_s, __popc(mask));
-      base = __shfl_sync(0xffffffffu, base, 0) + __popc(mask & ((1u << lane) - 1u));
-      if (keep && base < SEL_LIST)
-        list[base] = ((unsigned long long)key << 32) | (0xffffffffu - (uint32_t)m);
+  for (int m0 = 0; m0 < Ci; m0 += 4 * SEL_THREADS) {
+    const int m = m0 + 4 * tid;
+    float v[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    if (m + 4 <= Ci) {
+      const float4 x = *reinterpret_cast<const float4*>(vals + m);
+      v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (m + k < Ci) v[k] = vals[m + k];
+    }
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      sum += exp2f((v[k] - mx) * LOG2E);
+      n += m + k < Ci && score_key(v[k]) >= bound;
+    }
+    if (n > 0) {
+      int at = atomicAdd(&cnt_s, n);  // the list's order does not matter: keys are ranked below
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t key = score_key(v[k]);
+        if (m + k < Ci && key >= bound && at < SEL_LIST)
+          list[at++] = ((unsigned long long)key << 32) | (0xffffffffu - (uint32_t)(m + k));
+      }
     }
   }
   const float lse = mx + logf(block_sum(sum, red));  // its barriers also close the list
@@ -405,6 +428,9 @@ __global__ void __launch_bounds__(SEL_THREADS) k_tree_select(TreeArgs a, TreeWs 
   } else if (kk > 0) {
     const int per = ((Ci + SEL_THREADS - 1) / SEL_THREADS) | 1;  // odd: no bank conflicts
     const int lo = min(tid * per, Ci), hi = min(lo + per, Ci);
+    uint32_t* keys = reinterpret_cast<uint32_t*>(vals);
+    for (int m = tid; m < Ci; m += SEL_THREADS) keys[m] = score_key(vals[m]);
+    __syncthreads();
     select_by_bits(keys, lo, hi, kk, scan, &th_s, &last_s);
     const uint32_t th = th_s;
     const int last = last_s;
@@ -448,7 +474,7 @@ static cudaError_t launch_typed(const TreeArgs& a, const TreeWs& w, cudaStream_t
   const size_t smem = (size_t)2 * T8 * (D + 16) * sizeof(float);
   cudaError_t e = ensure_smem(k_tree_scores<T, S, D>, smem);
   if (e != cudaSuccess) return e;
-  const size_t ksm = (size_t)(C + 1) * sizeof(uint32_t);
+  const size_t ksm = (size_t)(tree_stride(C) + 4) * sizeof(float);
   e = ensure_smem(k_tree_select<T, S, D>, ksm);
   if (e != cudaSuccess) return e;
   // summaries of a CTA: whole passes, and one wave of the CTAs that an SM holds
@@ -494,7 +520,7 @@ static size_t tree_carve(int B, int Hq, int Hkv, int T, int N, int d, int topk, 
   TreeWs t;
   t.ubits = reinterpret_cast<uint32_t*>(take(topk > 0 ? groups * words * 4 : 0));
   t.rows = reinterpret_cast<TreeRow*>(take(topk > 0 ? rows * sizeof(TreeRow) : 0));
-  t.scores = reinterpret_cast<float*>(take(topk > 0 ? rows * C * 4 : 0));
+  t.scores = reinterpret_cast<float*>(take(topk > 0 ? rows * tree_stride((int)C) * 4 : 0));
   t.ml = reinterpret_cast<float2*>(take(parts * sizeof(float2)));
   t.part = reinterpret_cast<float*>(take(parts * d * 4));
   if (w) *w = t;

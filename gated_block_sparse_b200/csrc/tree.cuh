@@ -133,12 +133,15 @@ __device__ __forceinline__ float tree_bias(const TreeRow& t, float score, int m,
   return keep ? (gated ? score - t.lse : 0.f) : -INFINITY;
 }
 
+// Scores of a row: C of them, rows 16 bytes aligned.
+__host__ __device__ __forceinline__ int tree_stride(int C) { return (C + 3) & ~3; }
+
 // Workspace of one call.
 struct TreeWs {
-  float* scores;    // [row][N / 64]
+  float* scores;    // [row][tree_stride(N / 64)]
   TreeRow* rows;    // [row]
   uint32_t* ubits;  // [group][words]: blocks that some token selected
-  float* part;      // [group][split][G T][d]: outputs before the division
+  float* part;      // [group][split][d / 4][G T][4]: outputs before the division
   float2* ml;       // [group][split][G T]: running maximum (log2 units) and sum
 };
 
@@ -173,6 +176,12 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src, bool full
 }
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// Column c of a row's partial output, from the row's first four columns: the
+// rows of a warp write 16-byte pieces side by side.
+__device__ __forceinline__ size_t tree_part_at(int c, size_t R) {
+  return (size_t)(c >> 2) * R * 4 + (c & 3);
 }
 
 cudaError_t launch_tree_select(const TreeArgs& a, const TreeWs& w, int bf16, int sum_bf16, int d,
@@ -250,8 +259,8 @@ __device__ __forceinline__ int tree_units(const TreeArgs& a, const uint32_t* __r
         left -= pc;
       }
     }
-    __syncthreads();
   }
+  __syncthreads();
   u0 = (nu + 2) * split / a.ns;
   u1 = (nu + 2) * (split + 1) / a.ns;
   return nu;
