@@ -679,6 +679,7 @@ sas_status sas_device_status(int clear, sas_stream_t stream) {
       {"k_rotary", sas::rotary_error_word},
       {"k_page_*", sas::pages_error_word},
       {"k_append", sas::append_error_word},
+      {"k_tree_scores", sas::tree_scores_error_word},
       {"k_tree_select", sas::tree_select_error_word},
       {"k_tree_attn_simt", sas::tree_attn_error_word},
       {"k_tree_attn_tc", sas::tree_tc_error_word},

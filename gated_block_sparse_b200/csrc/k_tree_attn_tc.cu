@@ -98,13 +98,6 @@ __device__ __forceinline__ void sync_but_tma() {
   asm volatile("bar.sync 1, %0;" ::"n"(TT_THREADS - 32) : "memory");
 }
 
-// Offset of 16-byte piece p of row `row` in a K-major tile of `nrows` rows
-// under the 128-byte swizzle: 64-column chunks one after the other, rows of
-// 128 bytes, the piece's index within the row xor (row mod 8).
-__device__ __forceinline__ uint32_t sw_off(int row, int p, int nrows) {
-  return (uint32_t)((p >> 3) * nrows * 128 + row * 128 + (((p & 7) ^ (row & 7)) << 4));
-}
-
 struct RowState {
   unsigned long long anc, early;
   TreeRow info;

@@ -1,18 +1,11 @@
-// Block selection of drafted tokens: scores over the cached block summaries,
-// then gate and Top-K of every token's own row.
+// Block selection of drafted tokens: gate and Top-K of every token's own row
+// of scores (k_tree_scores.cu).
 //
-//   s_im = scale qbar_i . ksum_m, qbar_i the mean of the group's heads at
-//   token i, m < c0; for a token whose path has filled the tail's block, also
-//   s_i,c0 with the mean of that block's 64 keys (rounded to the summaries'
-//   type); log g = s - LSE(s); the topk best, ties to the lower block.
+//   log g = s - LSE(s) over the row's C_i blocks; the topk best are kept, ties
+//   to the lower block. A token whose path has filled the tail's block also
+//   scores that block, s_i,c0 = scale qbar_i . mean of its 64 keys (rounded to
+//   the summaries' type).
 //
-// k_tree_scores reads every summary once for all T tokens. The products are
-// tensor-core work (T x C x d multiply-adds: fp32 FMAs would take 14 us at
-// 512K and T = 64, where the summaries' bytes take 5), but the order of the
-// blocks needs fp32: each factor is split into two tf32 parts, x = hi + lo + e
-// with |e| <= 2^-22 |x|, and hi hi + hi lo + lo hi is accumulated in fp32
-// (bf16 summaries are tf32 values: one part). What is dropped is 2^-22 of a
-// product, below the fp32 accumulation's own rounding.
 // k_tree_select: one CTA per row.
 #include <math.h>
 
@@ -24,190 +17,6 @@
 namespace sas {
 
 __device__ uint32_t g_tree_select_err = 0;
-
-namespace {
-
-constexpr int TS_THREADS = 128;
-constexpr int TS_BLOCKS = 16 * (TS_THREADS / 32);  // summaries of a pass: 16 a warp
-
-// D += A B, m16n8k8: A[row][k], B[k][col] in tf32 (row-major, column-major
-// fragments), D in fp32.
-__device__ __forceinline__ void mma_tf32(float (&c)[4], const float (&a)[4], float b0, float b1) {
-  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(__float_as_uint(a[0])), "r"(__float_as_uint(a[1])), "r"(__float_as_uint(a[2])),
-        "r"(__float_as_uint(a[3])), "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)));
-}
-
-// The leading 11 significant bits of x (a tf32 value), and of what is left.
-__device__ __forceinline__ float tf32_hi(float x) {
-  return __uint_as_float(__float_as_uint(x) & 0xffffe000u);
-}
-
-// Four consecutive summary elements as loaded.
-template <typename S> struct Raw;
-template <> struct Raw<float> {
-  float4 v;
-  __device__ __forceinline__ void load(const float* p) {
-    v = __ldg(reinterpret_cast<const float4*>(p));
-  }
-  __device__ __forceinline__ float get(int i) const {
-    return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
-  }
-};
-template <> struct Raw<__nv_bfloat16> {
-  uint2 v;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
-    v = __ldg(reinterpret_cast<const uint2*>(p));
-  }
-  __device__ __forceinline__ float get(int i) const {
-    const uint32_t w = i < 2 ? v.x : v.y;
-    return __uint_as_float((i & 1) ? (w & 0xffff0000u) : (w << 16));
-  }
-};
-
-}  // namespace
-
-// One CTA per (stretch of summaries, kv group, sequence). A warp multiplies 16
-// summaries (rows of A, straight from global memory) with all tokens (columns
-// of B, in shared memory, split once). The order of the k index inside a group
-// of 16 is free as long as A and B share it: lane c of a quad takes elements
-// 4c .. 4c + 3, one 16-byte load, as k = c and c + 4 of two steps. Rows of
-// shared memory are D + 16 floats apart, so that those loads meet no bank twice.
-template <typename T, typename S, int D>
-__global__ void __launch_bounds__(TS_THREADS, 3) k_tree_scores(TreeArgs a, TreeWs w, int stretch) {
-  constexpr int LD = D + 16, VT = Vec16<T>::N, KG = D / 16;
-  constexpr bool SPLIT = sizeof(S) == 4;
-  extern __shared__ __align__(16) float sm_f[];
-  const int T8 = (a.T + 7) & ~7;
-  float* qh = sm_f;            // [T8][LD]
-  float* ql = sm_f + T8 * LD;  // [T8][LD]
-  const int r = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-  const int G = a.Hq / a.Hkv, C = a.N / SAS_BLOCK;
-  const int m_lo = blockIdx.x * stretch;
-  const size_t group = (size_t)b * a.Hkv + r;
-  grid_dep_wait();
-  grid_dep_launch();
-  for (int i = m_lo / 32 + tid; i < min((m_lo + stretch) / 32, a.words); i += TS_THREADS)
-    w.ubits[group * a.words + i] = 0u;
-  const int n = __ldg(a.lens + b), ntk = a.ntok ? __ldg(a.ntok + b) : a.T;
-  const int c0 = min(max(n, 0), a.N) / SAS_BLOCK, nt = min(max(ntk, 0), a.T);
-  const int m_hi = min(m_lo + stretch, c0);
-  if (m_lo >= m_hi || nt == 0) return;
-  // A of a pass: rows quad and quad + 8 of the warp's 16 (a row past the end
-  // reads the last one), loaded a pass ahead
-  const int quad = lane >> 2, c = lane & 3, ntiles = (nt + 7) >> 3;
-  const S* sums = static_cast<const S*>(a.ksum) + 4 * c;
-  auto row_at = [&](int m) -> size_t {
-    m = min(m, m_hi - 1);
-    return (a.table ? (size_t)tree_page(a, b, m, &g_tree_select_err) * a.Hkv + r : group * C + m) * D;
-  };
-  Raw<S> x[2][KG];
-  size_t at[2];
-  int m0 = m_lo + wid * 16;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    at[h] = row_at(m0 + quad + 8 * h);
-#pragma unroll
-    for (int g = 0; g < KG; ++g) x[h][g].load(sums + at[h] + 16 * g);
-    at[h] = row_at(m0 + TS_BLOCKS + quad + 8 * h);
-  }
-  const float inv_g = 1.0f / (float)G;
-#pragma unroll 2
-  for (int e = tid; e < T8 * (D / VT); e += TS_THREADS) {
-    const int row = e / (D / VT), col = (e % (D / VT)) * VT;
-    float s[VT];
-#pragma unroll
-    for (int i = 0; i < VT; ++i) s[i] = 0.f;
-    if (row < nt) {
-      const T* q = static_cast<const T*>(a.q) + (((size_t)b * a.Hq + r * G) * a.T + row) * D + col;
-#pragma unroll 4
-      for (int g = 0; g < G; ++g) {
-        float y[VT];
-        Vec16<T>::load_nc(q + (size_t)g * a.T * D, y);
-#pragma unroll
-        for (int i = 0; i < VT; ++i) s[i] += y[i];
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < VT; i += 4) {
-      float4 h, l;
-      const float m[4] = {s[i] * inv_g, s[i + 1] * inv_g, s[i + 2] * inv_g, s[i + 3] * inv_g};
-      h = make_float4(tf32_hi(m[0]), tf32_hi(m[1]), tf32_hi(m[2]), tf32_hi(m[3]));
-      l = make_float4(tf32_hi(m[0] - h.x), tf32_hi(m[1] - h.y), tf32_hi(m[2] - h.z),
-                      tf32_hi(m[3] - h.w));
-      *reinterpret_cast<float4*>(qh + row * LD + col + i) = h;
-      *reinterpret_cast<float4*>(ql + row * LD + col + i) = l;
-    }
-  }
-  __syncthreads();
-  const int CS = tree_stride(C);
-  float* out = w.scores + group * a.T * CS;
-  for (; m0 < m_hi; m0 += TS_BLOCKS) {
-    float acc[TREE_MAX / 8][4];
-#pragma unroll
-    for (int j = 0; j < TREE_MAX / 8; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
-    const bool more = m0 + TS_BLOCKS < m_hi;
-#pragma unroll
-    for (int g = 0; g < KG; ++g) {
-      float hi[2][4], lo[2][4];  // of the two k steps of this group
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {  // fragment i: row half i & 1, k half i >> 1
-          const float v = x[i & 1][g].get(2 * k + (i >> 1));
-          hi[k][i] = SPLIT ? tf32_hi(v) : v;
-          lo[k][i] = SPLIT ? tf32_hi(v - hi[k][i]) : 0.f;
-        }
-      if (more) {  // this group's registers take the next pass's values
-#pragma unroll
-        for (int h = 0; h < 2; ++h) x[h][g].load(sums + at[h] + 16 * g);
-      }
-      // four token tiles at a time: consecutive MMAs go to different sums
-#pragma unroll
-      for (int j0 = 0; j0 < TREE_MAX / 8; j0 += 4) {
-        if (j0 >= ntiles) break;
-        float4 bh[4], bl[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (j0 + j < ntiles) {
-            const int o = (8 * (j0 + j) + quad) * LD + 16 * g + 4 * c;
-            bh[j] = *reinterpret_cast<const float4*>(qh + o);
-            bl[j] = *reinterpret_cast<const float4*>(ql + o);
-          }
-#define SAS_EACH(A, X, Y)              \
-  _Pragma("unroll") for (int j = 0; j < 4; ++j) if (j0 + j < ntiles) \
-      mma_tf32(acc[j0 + j], A, X, Y)
-        SAS_EACH(hi[0], bl[j].x, bl[j].y);
-        SAS_EACH(hi[1], bl[j].z, bl[j].w);
-        if (SPLIT) {
-          SAS_EACH(lo[0], bh[j].x, bh[j].y);
-          SAS_EACH(lo[1], bh[j].z, bh[j].w);
-        }
-        SAS_EACH(hi[0], bh[j].x, bh[j].y);
-        SAS_EACH(hi[1], bh[j].z, bh[j].w);
-#undef SAS_EACH
-      }
-    }
-    if (more) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) at[h] = row_at(m0 + 2 * TS_BLOCKS + quad + 8 * h);
-    }
-    float* o = out + (size_t)(2 * c) * CS + m0 + quad;
-#pragma unroll
-    for (int j = 0; j < TREE_MAX / 8; ++j) {
-      if (j < ntiles) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)  // row quad + 8 (i >> 1), column 2 c + (i & 1)
-          if (8 * j + 2 * c + (i & 1) < nt && m0 + quad + 8 * (i >> 1) < m_hi)
-            o[(size_t)(8 * j + (i & 1)) * CS + 8 * (i >> 1)] = acc[j][i] * a.scale + 0.f;
-      }
-    }
-  }
-}
 
 namespace {
 constexpr int SEL_THREADS = 256;
@@ -470,25 +279,10 @@ __global__ void __launch_bounds__(SEL_THREADS) k_tree_select(TreeArgs a, TreeWs 
 // ------------------------------------------------------------------ host
 template <typename T, typename S, int D>
 static cudaError_t launch_typed(const TreeArgs& a, const TreeWs& w, cudaStream_t st) {
-  const int C = a.N / SAS_BLOCK, T8 = (a.T + 7) & ~7;
-  const size_t smem = (size_t)2 * T8 * (D + 16) * sizeof(float);
-  cudaError_t e = ensure_smem(k_tree_scores<T, S, D>, smem);
+  const size_t smem = (size_t)(tree_stride(a.N / SAS_BLOCK) + 4) * sizeof(float);
+  cudaError_t e = ensure_smem(k_tree_select<T, S, D>, smem);
   if (e != cudaSuccess) return e;
-  const size_t ksm = (size_t)(tree_stride(C) + 4) * sizeof(float);
-  e = ensure_smem(k_tree_select<T, S, D>, ksm);
-  if (e != cudaSuccess) return e;
-  // summaries of a CTA: whole passes, and one wave of the CTAs that an SM holds
-  // (three by registers, fewer by shared memory)
-  const long long groups = (long long)a.B * a.Hkv;
-  const long long room = 148 * (smem > 75 * 1024 ? 2 : 3);
-  long long per_group = room / groups;
-  if (per_group < 1) per_group = 1;
-  long long stretch = (C + per_group - 1) / per_group;
-  stretch = (stretch + TS_BLOCKS - 1) / TS_BLOCKS * TS_BLOCKS;
-  e = tree_launch(k_tree_scores<T, S, D>, dim3((unsigned)((C + stretch - 1) / stretch), a.Hkv, a.B),
-                  TS_THREADS, smem, st, a, w, (int)stretch);
-  if (e != cudaSuccess) return e;
-  return tree_launch(k_tree_select<T, S, D>, dim3(a.T, a.Hkv, a.B), SEL_THREADS, ksm, st, a, w);
+  return tree_launch(k_tree_select<T, S, D>, dim3(a.T, a.Hkv, a.B), SEL_THREADS, smem, st, a, w);
 }
 
 cudaError_t launch_tree_select(const TreeArgs& a, const TreeWs& w, int bf16, int sum_bf16, int d,
@@ -538,7 +332,9 @@ cudaError_t launch_tree(TreeArgs a, int bf16, int sum_bf16, int d, void* ws, cud
   a.ns = tree_splits(a.B, a.Hq, a.Hkv, a.T, a.N, a.topk, bf16);
   tree_carve(a.B, a.Hq, a.Hkv, a.T, a.N, d, a.topk, a.ns, static_cast<unsigned char*>(ws), &w);
   if (a.topk > 0) {
-    cudaError_t e = launch_tree_select(a, w, bf16, sum_bf16, d, st);
+    cudaError_t e = launch_tree_scores(a, w, bf16, sum_bf16, d, st);
+    if (e != cudaSuccess) return e;
+    e = launch_tree_select(a, w, bf16, sum_bf16, d, st);
     if (e != cudaSuccess) return e;
   }
   return bf16 ? launch_tree_attn_tc(a, w, d, st) : launch_tree_attn_simt(a, w, d, st);

@@ -217,6 +217,7 @@ struct TreeArgs {
 int tree_splits(int B, int Hq, int Hkv, int T, int N, int topk, int bf16);
 size_t tree_ws_bytes(int B, int Hq, int Hkv, int T, int N, int d, int topk, int bf16);
 cudaError_t launch_tree(TreeArgs a, int bf16, int sum_bf16, int d, void* ws, cudaStream_t st);
+uint32_t* tree_scores_error_word();
 uint32_t* tree_select_error_word();
 uint32_t* tree_attn_error_word();
 uint32_t* tree_tc_error_word();

@@ -184,6 +184,8 @@ __device__ __forceinline__ size_t tree_part_at(int c, size_t R) {
   return (size_t)(c >> 2) * R * 4 + (c & 3);
 }
 
+cudaError_t launch_tree_scores(const TreeArgs& a, const TreeWs& w, int bf16, int sum_bf16, int d,
+                               cudaStream_t st);
 cudaError_t launch_tree_select(const TreeArgs& a, const TreeWs& w, int bf16, int sum_bf16, int d,
                                cudaStream_t st);
 cudaError_t launch_tree_attn_simt(const TreeArgs& a, const TreeWs& w, int d, cudaStream_t st);
@@ -210,6 +212,13 @@ __device__ __forceinline__ TreeRow tree_row(const TreeArgs& a, const TreeWs& w, 
   t.last = -1;
   t.tail_bias = s.tail + tree_depth(anc) >= SAS_BLOCK ? -INFINITY : 0.f;
   return t;
+}
+
+// Offset of 16-byte piece p of row `row` in a K-major bf16 tile of `nrows`
+// rows under the 128-byte swizzle: 64-column chunks one after the other, rows
+// of 128 bytes, the piece's index within the row xor (row mod 8).
+__device__ __forceinline__ uint32_t sw_off(int row, int p, int nrows) {
+  return (uint32_t)((p >> 3) * nrows * 128 + row * 128 + (((p & 7) ^ (row & 7)) << 4));
 }
 
 // The units of one split of a (sequence, kv group): the blocks that some
