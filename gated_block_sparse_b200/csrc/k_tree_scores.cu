@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(SC_THREADS, scores_ctas<S, D>()) k_tree_scores
   }
   // B: qbar in three parts, zeros behind the last token
   const float inv_g = 1.0f / (float)G;
-#pragma unroll 2
+#pragma unroll (NP == 3 ? 4 : 2)
   for (int e = tid; e < NT * PC; e += SC_THREADS) {
     const int row = e / PC, p = e % PC;
     float s[8];

@@ -21,6 +21,7 @@ __device__ uint32_t g_tree_select_err = 0;
 namespace {
 constexpr int SEL_THREADS = 256;
 constexpr int SEL_WARPS = SEL_THREADS / 32;
+constexpr int SEL_BUCKETS = SEL_THREADS;  // one a thread
 constexpr int SEL_LIST = 512;  // candidates ranked by counting
 constexpr float LOG2E = 1.4426950408889634f;
 }  // namespace
@@ -90,10 +91,13 @@ __global__ void __launch_bounds__(SEL_THREADS) k_tree_select(TreeArgs a, TreeWs 
   __shared__ TreeShared tree;
   __shared__ float red[SEL_WARPS];
   __shared__ uint32_t scan[SEL_WARPS];
-  __shared__ float part[SEL_THREADS];
+  __shared__ float part[SEL_THREADS * 8];  // at most 8 columns of a key a thread
+  __shared__ int path[SAS_BLOCK];
+  __shared__ float red2[SEL_WARPS];
+  __shared__ int hist[SEL_BUCKETS];
   __shared__ __align__(16) unsigned long long list[SEL_LIST];
-  __shared__ int kept[128];
-  __shared__ int cnt_s, last_s;
+  __shared__ __align__(16) int kept[128];
+  __shared__ int cnt_s, last_s, bucket_s, many_s;
   __shared__ uint32_t th_s;
   const int i = blockIdx.x, r = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
   const int lane = tid & 31, wid = tid >> 5;
@@ -111,35 +115,43 @@ __global__ void __launch_bounds__(SEL_THREADS) k_tree_select(TreeArgs a, TreeWs 
   const int kk = min(a.topk, Ci);
   float virt = 0.f;
   if (crossed) {
-    // mean key of the tail's block as this path fills it: thread (part, column)
-    // sums every P-th key, the tail's first, then the path's in their order
-    constexpr int P = SEL_THREADS / D;
-    const int c = tid % D, p = tid / D;
-    const T* kc = static_cast<const T*>(a.kc);
+    // Mean key of the tail's block as this path fills it: the tail's keys, then
+    // the path's first ones. Thread (group, piece) sums every GRP-th key of one
+    // 16-byte piece, all its loads in flight; the groups meet in shared memory.
+    constexpr int VT = Vec16<T>::N, PIECES = D / VT, GRP = SEL_THREADS / PIECES;
+    const int pc = (tid % PIECES) * VT, g = tid / PIECES;
+    if (tid < TREE_MAX && (anc >> tid & 1ull)) {
+      const int at = s.tail + __popcll(anc & ((1ull << tid) - 1ull));
+      if (at < SAS_BLOCK) path[at] = tid;
+    }
+    __syncthreads();
+    const T* kc = static_cast<const T*>(a.kc) +
+                  (s.tail > 0 ? tree_block_row(a, b, r, s.c0, &g_tree_select_err) * D : 0);
     const T* kd = static_cast<const T*>(a.kd) + group * a.T * D;
-    float sum = 0.f;
-    if (s.tail > 0) {
-      const size_t base = tree_block_row(a, b, r, s.c0, &g_tree_select_err);
-#pragma unroll 8
-      for (int j = p; j < s.tail; j += P) sum += to_f(kc[(base + j) * D + c]);
+    float sum[VT];
+#pragma unroll
+    for (int e = 0; e < VT; ++e) sum[e] = 0.f;
+#pragma unroll
+    for (int k = 0; k < SAS_BLOCK / GRP; ++k) {
+      const int j = g + k * GRP;
+      float y[VT];
+      Vec16<T>::load_nc((j < s.tail ? kc + (size_t)j * D : kd + (size_t)path[j] * D) + pc, y);
+#pragma unroll
+      for (int e = 0; e < VT; ++e) sum[e] += y[e];
     }
-    unsigned long long rest = anc;
-    for (int n = 0; n < SAS_BLOCK - s.tail; ++n) {
-      const int j = __ffsll((long long)rest) - 1;
-      rest &= rest - 1;
-      if ((n % P) == p) sum += to_f(kd[(size_t)j * D + c]);
-    }
-    part[tid] = sum;
+#pragma unroll
+    for (int e = 0; e < VT; ++e) part[g * D + pc + e] = sum[e];
     __syncthreads();
     float dot = 0.f;
     if (tid < D) {
+      float qb = 0.f;
+#pragma unroll 4
+      for (int h = 0; h < G; ++h)
+        qb += to_f(static_cast<const T*>(a.q)[(((size_t)b * a.Hq + r * G + h) * a.T + i) * D + tid]);
       float mean = 0.f;
 #pragma unroll
-      for (int k = 0; k < P; ++k) mean += part[k * D + tid];
+      for (int k = 0; k < GRP; ++k) mean += part[k * D + tid];
       mean = to_f(from_f<S>(mean * (1.0f / SAS_BLOCK)));
-      float qb = 0.f;
-      for (int g = 0; g < G; ++g)
-        qb += to_f(static_cast<const T*>(a.q)[(((size_t)b * a.Hq + r * G + g) * a.T + i) * D + tid]);
       dot = qb * (1.0f / (float)G) * mean;
     }
     virt = block_sum(dot, red) * a.scale;
@@ -149,6 +161,8 @@ __global__ void __launch_bounds__(SEL_THREADS) k_tree_select(TreeArgs a, TreeWs 
     last_s = -1;
     th_s = 0xffffffffu;
   }
+  hist[tid] = 0;
+  if (tid < 128) kept[tid] = 0x7fffffff;
   grid_dep_wait();
   // Scores: four at a time into shared memory, with the thread's maximum; the
   // tail's block last.
@@ -163,24 +177,74 @@ __global__ void __launch_bounds__(SEL_THREADS) k_tree_select(TreeArgs a, TreeWs 
     *reinterpret_cast<float4*>(vals + m) = v;
     mx = fmaxf(mx, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
   }
-  const uint32_t best = mx > -INFINITY ? score_key(mx) : 0u;  // a subset's keys bound the set's
+  // A lower bound of the kk-th best score: that of the threads' own maxima (a
+  // subset), by buckets of equal width between the least and the largest of
+  // them. bucket() never decreases, so every score of the kk best lies in the
+  // bound's bucket or above; a score that is not finite does too.
+  const float best = mx;
+  float mn = mx > -INFINITY ? mx : INFINITY;
   mx = warp_max(mx);
-  if (lane == 0) red[wid] = mx;
+  mn = -warp_max(-mn);
+  if (lane == 0) {
+    red[wid] = mx;
+    red2[wid] = mn;
+  }
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < SEL_WARPS; ++k) mx = fmaxf(mx, red[k]);
+  for (int k = 0; k < SEL_WARPS; ++k) {
+    mx = fmaxf(mx, red[k]);
+    mn = fminf(mn, red2[k]);
+  }
   if (crossed) {
-    mx = fmaxf(mx, virt);
     if (tid == 0) vals[s.c0] = virt;
   }
-  // A lower bound of the kk-th best key: that of the threads' own best ones (a
-  // subset), by its upper 16 bits.
-  uint32_t bound = 0;
-#pragma unroll 1
-  for (int bit = 31; bit >= 16; --bit) {
-    const uint32_t cand = bound | (1u << bit);
-    if (__syncthreads_count(best >= cand) >= kk) bound = cand;
+  // A few scores far above the rest leave the rest in few buckets: a bound whose
+  // bucket holds many of the maxima is sought again inside that bucket (any
+  // map that never decreases will do).
+  float width = (mx - mn) * (1.0f / SEL_BUCKETS), inv_w = 0.f;
+  auto bucket = [&](float v) { return fminf((v - mn) * inv_w, (float)(SEL_BUCKETS - 1)); };
+  for (int pass = 0;; ++pass) {
+    inv_w = width > 1e-30f && width < INFINITY ? 1.0f / width : 0.f;
+    if (best > -INFINITY) atomicAdd(&hist[(int)fmaxf(bucket(best), 0.f)], 1);
+    __syncthreads();
+    if (wid == 0) {  // lane l: buckets 8 l .. 8 l + 7, counted from the top
+      constexpr int PER = SEL_BUCKETS / 32;
+      int c[PER], own = 0;
+#pragma unroll
+      for (int k = 0; k < PER; ++k) own += c[k] = hist[lane * PER + k];
+      int above = own;  // of this lane and the higher ones
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_down_sync(0xffffffffu, above, o);
+        if (lane + o < 32) above += y;
+      }
+      if (lane == 0) {  // fewer maxima than kk: every score is a candidate
+        bucket_s = 0;
+        many_s = 0;
+      }
+      __syncwarp();
+      int run = above - own;
+      if (run < kk && above >= kk) {
+#pragma unroll
+        for (int k = PER - 1; k >= 0; --k) {
+          const int before = run;
+          run += c[k];
+          if (before < kk && run >= kk) {
+            bucket_s = lane * PER + k;
+            many_s = c[k] > 32;
+          }
+        }
+      }
+    }
+    __syncthreads();
+    if (!many_s || pass == 2 || inv_w == 0.f) break;
+    mn += (float)bucket_s * width;
+    width *= 1.0f / SEL_BUCKETS;
+    hist[tid] = 0;
+    __syncthreads();
   }
+  if (crossed) mx = fmaxf(mx, virt);
+  const float bound = bucket_s > 0 ? (float)bucket_s : -INFINITY;
   // The sum of the gate's softmax, and the list of the keys at or above the bound.
   float sum = 0.f;
   for (int m0 = 0; m0 < Ci; m0 += 4 * SEL_THREADS) {
@@ -198,15 +262,15 @@ __global__ void __launch_bounds__(SEL_THREADS) k_tree_select(TreeArgs a, TreeWs 
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       sum += exp2f((v[k] - mx) * LOG2E);
-      n += m + k < Ci && score_key(v[k]) >= bound;
+      n += m + k < Ci && !(bucket(v[k]) < bound);
     }
     if (n > 0) {
       int at = atomicAdd(&cnt_s, n);  // the list's order does not matter: keys are ranked below
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const uint32_t key = score_key(v[k]);
-        if (m + k < Ci && key >= bound && at < SEL_LIST)
-          list[at++] = ((unsigned long long)key << 32) | (0xffffffffu - (uint32_t)(m + k));
+        if (m + k < Ci && !(bucket(v[k]) < bound) && at < SEL_LIST)
+          list[at++] = ((unsigned long long)score_key(v[k]) << 32) |
+                       (0xffffffffu - (uint32_t)(m + k));
       }
     }
   }
@@ -231,7 +295,11 @@ __global__ void __launch_bounds__(SEL_THREADS) k_tree_select(TreeArgs a, TreeWs 
     if (a.idx_out && tid < kk) {  // ascending: a block's place is the number of smaller ones
       const int m = kept[tid];
       int at = 0;
-      for (int e = 0; e < kk; ++e) at += kept[e] < m;
+#pragma unroll 4
+      for (int e = 0; e < kk; e += 4) {  // behind the last: no block's number
+        const int4 o = *reinterpret_cast<const int4*>(kept + e);
+        at += (o.x < m) + (o.y < m) + (o.z < m) + (o.w < m);
+      }
       a.idx_out[row * a.topk + at] = m;
     }
   } else if (kk > 0) {

@@ -500,6 +500,31 @@ def test_decode_tree_ties_go_to_the_lower_block(dtype, N, topk):
     assert (idx.cpu() == torch.tensor(want, dtype=torch.int32)).all()
 
 
+@pytest.mark.parametrize("spread", [1.0, 1e3, 1e6])
+def test_decode_tree_selects_beside_far_outliers(spread):
+    """A few blocks score far above the others (up to a million times their
+    spread): the kept set is still that of a stable sort. Scores are exact
+    here: one nonzero element a query and distinct summaries on a 2^-8 grid."""
+    B, Hkv, d, T, C, topk = 1, 2, 64, 5, 6000, 40
+    rng = np.random.Generator(np.random.PCG64(int(spread)))
+    q = torch.zeros((B, Hkv, T, d))
+    q[..., 3] = 1.0
+    lev = np.stack([rng.permutation(C) for _ in range(Hkv)]).astype(np.float64) / 256.0
+    for r in range(Hkv):
+        lev[r, rng.choice(C, 3, replace=False)] += 32.0 * spread
+    ks = torch.zeros((B, Hkv, C, d))
+    ks[0, :, :, 3] = torch.from_numpy(lev).float()
+    kd = torch.zeros((B, Hkv, T, d))
+    kc = torch.zeros((B, Hkv, C * 64, d))
+    idx = torch.full((B, Hkv, T, topk), -7, dtype=torch.int32, device=DEV)
+    sas.sas_decode_tree(q.to(DEV), kd.to(DEV), kd.to(DEV), kc.to(DEV), kc.to(DEV), i32([C * 64 - 64]),
+                        ks.to(DEV), topk, scale=1.0, idx_out=idx)
+    lev32 = ks[0, :, :C - 1, 3].numpy()  # one block is not whole yet
+    for r in range(Hkv):
+        want = np.sort(np.argsort(-lev32[r], kind="stable")[:topk])
+        assert (idx[0, r].cpu().numpy() == want).all()
+
+
 def test_decode_tree_of_one_token_is_a_decode_step():
     """T = 1 against sas_decode on the cache with the token appended; the same
     definition on two kernels, each within the tree's bound of it."""
