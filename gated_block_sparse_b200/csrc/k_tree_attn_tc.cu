@@ -13,6 +13,11 @@
 //              buffers) and O += P_j V_j (A = P_j read from TMEM);
 //   warps 0-3  softmax, thread i = row i = TMEM lane i; warps whose rows are
 //              all past the end take no part.
+// With at most 64 (32) rows the tile holds two (four) copies of them, and each
+// copy's threads take the softmax of a half (quarter) of a unit's keys, with
+// zeros in the rest of their P: the chain from S to P, which bounds a unit, is
+// shorter, and the idle lanes do the work. The copies meet at the end, in
+// shared memory.
 // The tail and the drafted tokens, which end inside a tile, come first in
 // their split: all threads write them into the ring's stages with zeros
 // behind the last key (whatever the cache holds there, 0 * NaN would reach
@@ -98,6 +103,32 @@ __device__ __forceinline__ void sync_but_tma() {
   asm volatile("bar.sync 1, %0;" ::"n"(TT_THREADS - 32) : "memory");
 }
 
+// 32 lanes x 16 consecutive 32-bit columns.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+// n columns (16, 32 or 64) of this thread's lane.
+template <int N>
+__device__ __forceinline__ void tmem_row(uint32_t taddr, float (&z)[N]) {
+  if constexpr (N == 16) {
+    tmem_ld16(taddr, z);
+  } else {
+#pragma unroll
+    for (int c = 0; c < N / 32; ++c) tc::tmem_ld32(taddr + 32 * c, reinterpret_cast<float(&)[32]>(z[32 * c]));
+  }
+  tc::tmem_wait_ld();
+}
+
 struct RowState {
   unsigned long long anc, early;
   TreeRow info;
@@ -168,12 +199,13 @@ __device__ __noinline__ float2 repair_row(const TreeArgs& a, const TreeWs& w, co
 
 }  // namespace
 
-template <int D>
+template <int D, int COPIES>
 __global__ void __launch_bounds__(TT_THREADS, 2)
     k_tree_attn_tc(const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap, TreeArgs a, TreeWs w) {
   using L = Lay<D>;
   constexpr int PC = D / 8;  // 16-byte pieces of a row
+  constexpr int RT = 128 / COPIES, NC = 64 / COPIES;  // rows of a copy, keys of a thread
   extern __shared__ __align__(1024) unsigned char sm[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::BAR);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::BAR + NBAR * 8);
@@ -192,7 +224,7 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
   // the next one start
   if (a.topk == 0) grid_dep_wait();
   grid_dep_launch();
-  const int rows = G * s.nt, row0 = tile * 128;
+  const int rows = G * s.nt, row0 = tile * RT;
   if (row0 >= rows) {
     grid_dep_wait();
     return;
@@ -202,7 +234,9 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
     grid_dep_wait();
     return;
   }
-  const int nwarp = min(4, (rows - row0 + 31) / 32);  // softmax warps with rows
+  const int cw = min(RT / 32, (rows - row0 + 31) / 32);  // warps with rows, of a copy
+  const int nwarp = COPIES * cw;
+  const bool softmax = warp < 4 && warp % (RT / 32) < cw;
   if (tid == 0) {
     for (int i = 0; i < NBAR; ++i) mbar_init(&bars[i], i == B_PF ? nwarp : 1);
     fence_mbar_init();
@@ -212,15 +246,16 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
     tc::prefetch_map(&kmap);
     tc::prefetch_map(&vmap);
   }
-  // Q: rows of the group's heads, zeros behind the last (only as far as the
-  // softmax warps look; other rows' products are never read)
+  // Q: rows of the group's heads, zeros behind the last
   const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
-  for (int e = warp == 5 ? 128 + lane : tid; warp != 4 && e < nwarp * 32 * PC;
+  for (int e = warp == 5 ? 128 + lane : tid; warp != 4 && e < cw * 32 * PC;
        e += TT_THREADS - 32) {
     const int row = e / PC, p = e % PC, gr = min(row0 + row, rows - 1);
-    cp_async16(sm + L::Q + sw_off(row, p, 128),
-               q + (((size_t)b * a.Hq + r * G + gr / s.nt) * a.T + gr % s.nt) * D + p * 8,
-               row0 + row < rows);
+    const __nv_bfloat16* src =
+        q + (((size_t)b * a.Hq + r * G + gr / s.nt) * a.T + gr % s.nt) * D + p * 8;
+#pragma unroll
+    for (int c = 0; c < COPIES; ++c)
+      cp_async16(sm + L::Q + sw_off(c * RT + row, p, 128), src, row0 + row < rows);
   }
   grid_dep_wait();
   int u0, u1;
@@ -231,7 +266,7 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
   const bool has_draft = u0 <= nu + 1 && nu + 1 < u1;
   const int nsp = (int)has_tail + (int)has_draft;
   const int nh = max(0, min(u1, nu) - u0), nunits = nsp + nh;
-  const size_t R = (size_t)G * a.T, prow = (group * a.ns + split) * R + row0 + tid;
+  const size_t R = (size_t)G * a.T, prow = (group * a.ns + split) * R + row0 + tid % RT;
   const int start = nh > 0 ? start_s : 0;
   if (warp == 4) {
     // ---------------------------------------------------------------- producer
@@ -290,13 +325,16 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
   const uint32_t tm_s[2] = {tmem, tmem + 64};
   const uint32_t tm_o = tmem + 128;
   if (nunits == 0) {  // more splits than units
-    if (tid < 128 && row0 + tid < rows) w.ml[prow] = make_float2(-1e30f, 0.f);
+    if (tid < RT && row0 + tid < rows) w.ml[prow] = make_float2(-1e30f, 0.f);
   } else if (warp == 5) {
     // ---------------------------------------------------------------- MMA issuer
     if (lane == 0) {
       constexpr uint32_t ID_QK = tc::idesc_bf16(128, 64, 0, 0);
       constexpr uint32_t ID_PV = tc::idesc_bf16(128, D, 0, 1);
-      const uint32_t q_addr = smem_u32(sm + L::Q);
+      // a step along an operand moves its descriptor's address field (16-byte units)
+      const uint64_t q_desc = tc::sw128_desc(smem_u32(sm + L::Q), 16, 1024);
+      const uint64_t k_desc = tc::sw128_desc(smem_u32(sm + L::KV), 16, 1024);
+      const uint64_t v_desc = tc::sw128_desc(smem_u32(sm + L::KV) + L::TILE, 8192, 1024);
       for (int j = 0; j < nsp; ++j) {  // written above
         mbar_arrive(&bars[B_KF + j]);
         mbar_arrive(&bars[B_VF + j]);
@@ -305,11 +343,11 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
         mbar_wait(&bars[B_PF], j & 1, err);
         mbar_wait_data(&bars[B_VF + (j & 1)], (j >> 1) & 1, err);
         tc::fence_after_sync();
-        const uint32_t v_addr = smem_u32(sm + L::KV + (j & 1) * 2 * L::TILE + L::TILE);
+        const uint64_t vd = v_desc + (((j & 1) * 2 * L::TILE) >> 4);
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {  // P_j: columns 8 ks .. 8 ks + 7 of S_j's buffer
-          const uint64_t bd = tc::sw128_desc(v_addr + ks * 2048, 8192, 1024);
-          mma_tmem_a(tm_o, tm_s[j & 1] + 8 * ks, bd, ID_PV, (j > 0 || ks > 0) ? 1u : 0u);
+          mma_tmem_a(tm_o, tm_s[j & 1] + 8 * ks, vd + ((ks * 2048) >> 4), ID_PV,
+                     (j > 0 || ks > 0) ? 1u : 0u);
         }
         tc::commit(&bars[B_OD]);
         tc::commit(&bars[B_VE + (j & 1)]);
@@ -320,13 +358,12 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
         // S_j overwrites P_{j-2} (S_{j-2}'s buffer): PV_{j-2} must have read it
         if (j >= 2) mbar_wait(&bars[B_OD], (j - 2) & 1, err);
         tc::fence_after_sync();
-        const uint32_t k_addr = smem_u32(sm + L::KV + st * 2 * L::TILE);
+        const uint64_t kd = k_desc + ((st * 2 * L::TILE) >> 4);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {  // K = D in steps of 16 (32 bytes)
           const uint32_t c = ks >> 2, off = (ks & 3) * 32;
-          const uint64_t ad = tc::sw128_desc(q_addr + c * 16384 + off, 16, 1024);
-          const uint64_t bd = tc::sw128_desc(k_addr + c * 8192 + off, 16, 1024);
-          tc::mma_bf16(tm_s[st], ad, bd, ID_QK, ks > 0 ? 1u : 0u);
+          tc::mma_bf16(tm_s[st], q_desc + ((c * 16384 + off) >> 4), kd + ((c * 8192 + off) >> 4),
+                       ID_QK, ks > 0 ? 1u : 0u);
         }
         tc::commit(&bars[B_SF + st]);
         tc::commit(&bars[B_KE + st]);
@@ -334,9 +371,10 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
       }
       pv(nunits - 1);
     }
-  } else if (warp < nwarp) {
+  } else if (softmax) {
     // ---------------------------------------------------------------- softmax
-    const int row = row0 + tid;
+    const int copy = warp / (RT / 32), row = row0 + tid % RT;
+    const int key0 = copy * NC;  // this thread's keys of a unit
     const bool valid = row < rows;
     const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
     const float c1 = a.scale * LOG2E, inv_scale = 1.0f / a.scale;
@@ -347,11 +385,13 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
     rs.info = tree_row(a, w, s, group, rs.tok, rs.anc);
     const float* sc = w.scores + (group * a.T + rs.tok) * tree_stride(a.N / SAS_BLOCK);
     float m = -1e30f, l = 0.f;
-    int blk = start - 1;
-    float next_score = 0.f;
-    if (nh > 0) {  // the score of the next history unit is loaded a unit ahead
-      blk = start;
-      next_score = __ldcg(sc + blk);
+    // history units' blocks and scores, loaded two units ahead
+    int blk = start, blk1 = start;
+    float score = 0.f, score1 = 0.f;
+    if (nh > 0) score = __ldcg(sc + blk);
+    if (nh > 1) {
+      blk1 = tree_next(bits, a.words, blk + 1);
+      score1 = __ldcg(sc + blk1);
     }
     for (int j = 0; j < nunits; ++j) {
       const int st = j & 1;
@@ -363,35 +403,29 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
         see = is_tail ? (1ull << s.tail) - 1ull : rs.anc;
         if (rs.info.tail_bias == -INFINITY) see &= is_tail ? 0ull : ~rs.early;
       } else {
-        bias = tree_bias(rs.info, next_score, blk, a.gated) * LOG2E;
-        if (j + 1 < nunits) {
-          blk = tree_next(bits, a.words, blk + 1);
-          next_score = __ldcg(sc + blk);
+        bias = tree_bias(rs.info, score, blk, a.gated) * LOG2E;
+        blk = blk1;
+        score = score1;
+        if (j + 2 < nunits) {
+          blk1 = tree_next(bits, a.words, blk1 + 1);
+          score1 = __ldcg(sc + blk1);
         }
       }
       if (!valid) see = 0ull;
-      const bool dead = bias == -INFINITY || see == 0ull;  // the row sees none of the unit
+      see >>= key0;
+      if (NC < 64) see &= (1ull << (NC & 63)) - 1ull;
+      const bool dead = bias == -INFINITY || see == 0ull;  // the row sees none of these keys
       mbar_wait_data(&bars[B_SF + st], (j >> 1) & 1, err);
       tc::fence_after_sync();
-      float z[64];
-      {
-        float x[32], y[32];
-        tc::tmem_ld32(tm_s[st] + lane_off, x);
-        tc::tmem_ld32(tm_s[st] + lane_off + 32, y);
-        tc::tmem_wait_ld();
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          z[i] = x[i];
-          z[32 + i] = y[i];
-        }
-      }
+      float z[NC];
+      tmem_row<NC>(tm_s[st] + lane_off + key0, z);
       if (special) {
         // masked keys to -inf; keys that the path moved into the tail's block
         // get its gate, in units of the raw products
         const float g = rs.info.tail_bias == -INFINITY ? 0.f : rs.info.tail_bias * inv_scale;
-        const unsigned long long gate = is_tail ? ~0ull : rs.early;
+        const unsigned long long gate = is_tail ? ~0ull : rs.early >> key0;
 #pragma unroll
-        for (int i = 0; i < 64; ++i) {
+        for (int i = 0; i < NC; ++i) {
           if (gate >> i & 1ull) z[i] += g;
           if (!(see >> i & 1ull)) z[i] = -INFINITY;
         }
@@ -400,7 +434,7 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
 #pragma unroll
       for (int c = 0; c < 4; ++c) zm[c] = fmaxf(z[2 * c], z[2 * c + 1]);
 #pragma unroll
-      for (int i = 8; i < 64; i += 8) {
+      for (int i = 8; i < NC; i += 8) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) zm[c] = max3(zm[c], z[i + 2 * c], z[i + 2 * c + 1]);
       }
@@ -412,9 +446,9 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
       const float muse = grow ? mnew : m;
       const float off = bias - muse;
       float r0 = 0.f, r1 = 0.f;
-      uint32_t pk[32];
+      uint32_t pk[NC / 2];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
+      for (int i = 0; i < NC / 2; ++i) {
         float a0, a1;
         fma2c(a0, a1, z[2 * i], z[2 * i + 1], c1, off);
         const float p0 = tc::ex2(a0), p1 = tc::ex2(a1);
@@ -426,7 +460,7 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
       if (dead) {  // whatever the products were, NaN included
         rsum = 0.f;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) pk[i] = 0u;
+        for (int i = 0; i < NC / 2; ++i) pk[i] = 0u;
       }
       if (j > 0) {
         // PV_{j-1} done before O is rescaled. Waiting on every unit also keeps
@@ -455,7 +489,8 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
       {
         float pf[32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) pf[i] = __uint_as_float(pk[i]);
+        for (int i = 0; i < 32; ++i)  // zeros at the other copies' keys
+          pf[i] = copy == i / (NC / 2) ? __uint_as_float(pk[i % (NC / 2)]) : 0.f;
         tc::tmem_st32(tm_s[st] + lane_off, pf);
       }
       tc::tmem_wait_st();
@@ -468,21 +503,76 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
     tc::fence_after_sync();
     float* out = w.part + (group * a.ns + split) * R * D + (size_t)row * 4;
     bool bad = !(fabsf(l) < INFINITY);
+    if constexpr (COPIES == 1) {
 #pragma unroll 1
-    for (int c = 0; c < D / 32; ++c) {
-      float ov[32];
-      tc::tmem_ld32(tm_o + lane_off + 32 * c, ov);
-      tc::tmem_wait_ld();
-      if (valid) {
+      for (int c = 0; c < D / 32; ++c) {
+        float ov[32];
+        tc::tmem_ld32(tm_o + lane_off + 32 * c, ov);
+        tc::tmem_wait_ld();
+        if (valid) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) bad |= !(fabsf(ov[i]) < INFINITY);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<float4*>(out + tree_part_at(32 * c + 4 * i, R)) =
+                make_float4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
+        }
+      }
+    } else {
+      // The copies' O and sums through shared memory (every tile has been
+      // read): rows side by side, four columns a piece; then each copy's
+      // threads join D / COPIES columns of their row.
+      float4* so = reinterpret_cast<float4*>(sm + L::KV);
+      float4* sml = reinterpret_cast<float4*>(sm + L::Q);
+      const int rr = tid % RT;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        float ov[32];
+        tc::tmem_ld32(tm_o + lane_off + 32 * c, ov);
+        tc::tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < 32; ++i) bad |= !(fabsf(ov[i]) < INFINITY);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          *reinterpret_cast<float4*>(out + tree_part_at(32 * c + 4 * i, R)) =
+          so[(copy * (D / 4) + 8 * c + i) * RT + rr] =
               make_float4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
       }
+      sml[copy * RT + rr] = make_float4(m, l, bad ? 1.f : 0.f, 0.f);
+      asm volatile("bar.sync 2, %0;" ::"r"(nwarp * 32) : "memory");
+      float f[COPIES];
+      float4 x[COPIES];
+      m = -1e30f;
+      bad = false;
+#pragma unroll
+      for (int k = 0; k < COPIES; ++k) {
+        x[k] = sml[k * RT + rr];
+        m = fmaxf(m, x[k].x);
+        bad |= x[k].z != 0.f;
+      }
+      l = 0.f;
+#pragma unroll
+      for (int k = 0; k < COPIES; ++k) {
+        f[k] = tc::ex2(x[k].x - m);
+        l = fmaf(x[k].y, f[k], l);
+      }
+      if (valid && !bad) {
+#pragma unroll
+        for (int c = 0; c < D / 4 / COPIES; ++c) {
+          const int c4 = copy * (D / 4 / COPIES) + c;
+          float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int k = 0; k < COPIES; ++k) {
+            const float4 v = so[(k * (D / 4) + c4) * RT + rr];
+            y.x = fmaf(v.x, f[k], y.x);
+            y.y = fmaf(v.y, f[k], y.y);
+            y.z = fmaf(v.z, f[k], y.z);
+            y.w = fmaf(v.w, f[k], y.w);
+          }
+          *reinterpret_cast<float4*>(out + tree_part_at(4 * c4, R)) = y;
+        }
+      }
     }
-    if (valid) {
+    if (valid && copy == 0) {
       float2 ml = make_float2(m, l);
       if (bad)
         ml = repair_row<D>(a, w, s, rs, bits, b, r,
@@ -500,7 +590,7 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
 }
 
 // ------------------------------------------------------------------ host
-template <int D>
+template <int D, int COPIES>
 static cudaError_t launch_tc(const TreeArgs& a, const TreeWs& w, cudaStream_t st) {
   CUtensorMap km, vm;
   const int rpp = a.table ? SAS_BLOCK : a.N, planes = (a.table ? a.npages : a.B) * a.Hkv;
@@ -508,17 +598,25 @@ static cudaError_t launch_tc(const TreeArgs& a, const TreeWs& w, cudaStream_t st
       !make_tma_map_bf16_3d(&vm, a.vc, D, rpp, planes))
     return cudaErrorInvalidValue;
   const size_t smem = Lay<D>::BITS + (size_t)a.words * sizeof(uint32_t);
-  cudaError_t e = ensure_smem(k_tree_attn_tc<D>, smem);
+  cudaError_t e = ensure_smem(k_tree_attn_tc<D, COPIES>, smem);
   if (e != cudaSuccess) return e;
-  const int rows = a.Hq / a.Hkv * a.T, tiles = (rows + 127) / 128;
-  e = tree_launch(k_tree_attn_tc<D>, dim3(tiles * a.ns, a.Hkv, a.B), TT_THREADS, smem, st, km, vm,
-                  a, w);
+  const int rows = a.Hq / a.Hkv * a.T, rt = 128 / COPIES, tiles = (rows + rt - 1) / rt;
+  e = tree_launch(k_tree_attn_tc<D, COPIES>, dim3(tiles * a.ns, a.Hkv, a.B), TT_THREADS, smem, st,
+                  km, vm, a, w);
   if (e != cudaSuccess) return e;
   return launch_tree_join(a, w, 1, D, st);
 }
 
+// Copies of the rows in a tile: as many as fit.
+template <int D>
+static cudaError_t launch_rows(const TreeArgs& a, const TreeWs& w, cudaStream_t st) {
+  const int rows = a.Hq / a.Hkv * a.T;
+  if (rows <= 32) return launch_tc<D, 4>(a, w, st);
+  return rows <= 64 ? launch_tc<D, 2>(a, w, st) : launch_tc<D, 1>(a, w, st);
+}
+
 cudaError_t launch_tree_attn_tc(const TreeArgs& a, const TreeWs& w, int d, cudaStream_t st) {
-  return d == 128 ? launch_tc<128>(a, w, st) : launch_tc<64>(a, w, st);
+  return d == 128 ? launch_rows<128>(a, w, st) : launch_rows<64>(a, w, st);
 }
 
 uint32_t* tree_tc_error_word() {
