@@ -5,7 +5,9 @@
 Objects go to gated_block_sparse_b200/_build/ (git-ignored); the shared
 library is gated_block_sparse_b200/libsas.so, linked against the static CUDA
 runtime. A source is recompiled when it or any header is newer than its
-object.
+object. The serving calls' binding, csrc/py_serving.cpp, is built beside it
+into gated_block_sparse_b200/_serving.so with the host compiler and torch's
+headers; it links libsas.so.
 """
 from __future__ import annotations
 
@@ -16,12 +18,15 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsas.so")
+EXT_SRC = os.path.join(CSRC, "py_serving.cpp")
+EXT = os.path.join(PKG, "_serving.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -58,8 +63,30 @@ def _compile(src: str, obj: str, verbose: bool) -> str:
     return res.stderr
 
 
+def _build_binding(force: bool) -> None:
+    """Compile csrc/py_serving.cpp into _serving.so (a CPython module)."""
+    hdr = glob.glob(os.path.join(ROOT, "include", "*.h"))
+    if not force and not _stale(EXT, EXT_SRC, hdr):
+        return
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    inc = [os.path.join(base, "include"), os.path.join(base, "include/torch/csrc/api/include"),
+           os.path.join(cuda, "include"), sysconfig.get_paths()["include"],
+           os.path.join(ROOT, "include")]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    cmd += [a for d in inc for a in ("-isystem", d)]
+    cmd += [EXT_SRC, "-o", EXT, "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cuda",
+            "-ltorch_cpu", "-ltorch", "-lc10_cuda", "-lc10", "-L", PKG, "-l:libsas.so",
+            "-Wl,-rpath,$ORIGIN"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"{os.path.basename(EXT_SRC)} failed:\n{res.stdout}\n{res.stderr}")
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link libsas.so; returns its path."""
+    """Compile and link libsas.so and the binding; returns libsas.so's path."""
     os.makedirs(OUT_DIR, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     deps = _headers()
@@ -77,6 +104,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         res = subprocess.run(cmd, capture_output=True, text=True)
         if res.returncode != 0:
             raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
+    _build_binding(force)
     return LIB
 
 

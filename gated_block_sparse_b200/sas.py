@@ -9,7 +9,6 @@ fallback: if libsas.so is missing or no GPU is present, calls raise.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 
 import torch
@@ -476,80 +475,41 @@ def sas_debug_wait_timeout(stream=None) -> None:
 
 
 # ---------------------------------------------------------------- serving
-# The calls of include/sas_serving.h check what the C side cannot see: every
-# tensor's device, element type and shape. They run on the device of their
-# first tensor, whatever the current one is, and take outputs and workspace
-# from the stream that they launch on. Small steps are bound by this host
-# code, so it makes each check once and opens a stream or device context only
-# where the current one is another.
+# The calls of include/sas_serving.h. _serving.so (csrc/py_serving.cpp) checks
+# every tensor's device, element type, shape and layout, takes outputs and
+# workspace, and makes the C call on the current stream of the tensors' device,
+# whatever device is the current one.
+_ext = None
 
 
-# Handle of a device's current stream, without the Stream object around it
-# (0.1 us against 3 us of torch.cuda.current_stream).
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+def _serving():
+    """The binding of the serving calls (built in-tree beside libsas.so)."""
+    global _ext
+    if _ext is None:
+        load_library()
+        try:
+            from gated_block_sparse_b200 import _serving as ext
+        except ImportError as e:
+            raise RuntimeError(f"_serving.so cannot be loaded ({e}): run "
+                               "`python -m gated_block_sparse_b200.build`") from e
+        _ext = ext
+    return _ext
 
 
-def _like(t):
-    """An uninitialised contiguous tensor of t's shape, type and device."""
-    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
+def _raise(fn: str, status: int, msg: str) -> None:
+    raise SasError(fn, status, msg)
 
 
-def _placed(fn):
-    """Run fn on its first tensor's device and, when given, on `stream`."""
-    @functools.wraps(fn)
-    def call(t, *args, stream=None, **kw):
-        dev = t.get_device()
-        if dev < 0:
-            raise ValueError("tensors must all be on one CUDA device")
-        if stream is not None:
-            if stream.device.index != dev:
-                raise ValueError(f"stream is on {stream.device}, the tensors are on {t.device}")
-            with torch.cuda.stream(stream):
-                return fn(t, *args, **kw)
-        if dev != torch.cuda.current_device():
-            with torch.cuda.device(dev):
-                return fn(t, *args, **kw)
-        return fn(t, *args, **kw)
-    return call
+def _on_stream(fn, stream, t, *args):
+    """fn(t, *args) on `stream`, which must be of t's device."""
+    if t.is_cuda and stream.device != t.device:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on {t.device}")
+    with torch.cuda.stream(stream):
+        return fn(t, *args)
 
 
-def _refuse(t, name, dtype, shape, dev):
-    if t.get_device() != dev:
-        raise ValueError(f"tensors must all be on one CUDA device ({name} is on {t.device})")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
-    raise ValueError(f"{name} must be contiguous")
-
-
-def _arg(t, name: str, dtype, shape, dev: int) -> int | None:
-    """Pointer of a contiguous tensor of this type and shape (None passes)."""
-    if t is None:
-        return None
-    if (t.get_device() != dev or t.dtype is not dtype or t.shape != shape
-            or not t.is_contiguous()):
-        _refuse(t, name, dtype, shape, dev)
-    return t.data_ptr()
-
-
-def _strided(t, name: str, dtype, shape, dev: int):
-    """Pointer and element strides {batch, head, token} (None: contiguous) of a
-    tensor whose rows are contiguous."""
-    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape:
-        _refuse(t, name, dtype, shape, dev)
-    if t.is_contiguous():
-        return t.data_ptr(), None
-    s = t.stride()
-    if s[3] != 1:
-        raise ValueError(f"the rows of {name} must be contiguous")
-    return t.data_ptr(), (ctypes.c_int64 * 3)(s[0], s[1], s[2])
-
-
-@_placed
 def sas_rotary(q, inv_freq, k=None, pos=None, start=None, parents=None, interleaved: bool = False,
-               amplitude: float = 1.0, inverse: bool = False, out=None):
+               amplitude: float = 1.0, inverse: bool = False, out=None, stream=None):
     """Rotary positions of q [B][Hq][N][d] and k [B][Hkv][N][d]; returns qo, or (qo, ko).
 
     q and k may be strided views (a fused projection's) with contiguous rows.
@@ -559,59 +519,34 @@ def sas_rotary(q, inv_freq, k=None, pos=None, start=None, parents=None, interlea
     transpose: it takes the gradients of the outputs to those of the inputs.
     out: qo, or (qo, ko); q and k themselves rotate in place.
     """
-    B, Hq, N, d = shape = q.shape
-    dev, dtype, i32 = q.get_device(), q.dtype, torch.int32
-    dt = _dt(q)
-    if out is None:
-        qo, ko = _like(q), None if k is None else _like(k)
-    else:
-        qo, ko = (out, None) if k is None else out
-    pq, sq = _strided(q, "q", dtype, shape, dev)
-    pqo, sqo = _strided(qo, "qo", dtype, shape, dev)
-    Hkv = 0
-    pk = sk = pko = sko = None
-    if k is not None:
-        Hkv = k.shape[1]
-        shape = (B, Hkv, N, d)
-        pk, sk = _strided(k, "k", dtype, shape, dev)
-        pko, sko = _strided(ko, "ko", dtype, shape, dev)
-    half = inv_freq.numel()
-    _check("sas_rotary", load_library().sas_rotary(
-        pq, sq, pqo, sqo, Hq, pk, sk, pko, sko, Hkv, dt, B, N, d,
-        _arg(inv_freq, "inv_freq", torch.float32, (half,), dev), 2 * half, interleaved, amplitude,
-        inverse, _arg(pos, "pos", i32, (B, N), dev), _arg(start, "start", i32, (B,), dev),
-        _arg(parents, "parents", i32, (B, N), dev), _raw_stream(dev)))
-    return qo if k is None else (qo, ko)
+    qo, ko = (None, None) if out is None else (out, None) if k is None else out
+    fn = _serving().rotary
+    if stream is None:
+        return fn(q, inv_freq, k, pos, start, parents, interleaved, amplitude, inverse, qo, ko)
+    return _on_stream(fn, stream, q, inv_freq, k, pos, start, parents, interleaved, amplitude,
+                      inverse, qo, ko)
 
 
-@_placed
-def sas_page_map(lens, nnew, block_table, free_pages, free_head, T: int, npages: int, out=None):
+def sas_page_map(lens, nnew, block_table, free_pages, free_head, T: int, npages: int, out=None,
+                 stream=None):
     """Pages and slots of nnew [B] <= T new tokens after lens [B] cached ones.
 
     Takes pages from free_pages[free_head:] into block_table [B][width] (in
     place) and returns (slots [B][T], new_lens [B], taken [B], head [1]), all
     int32. out supplies the four; new_lens may be lens and head free_head.
     """
-    i32, dev = torch.int32, lens.get_device()
-    B, width, nfree = lens.shape[0], block_table.shape[1], free_pages.numel()
-    if out is None:
-        out = (lens.new_empty((B, T)), _like(lens), _like(lens), _like(free_head))
-    slots, new_lens, taken, head = out
-    _check("sas_page_map", load_library().sas_page_map(
-        _arg(lens, "lens", i32, (B,), dev), _arg(nnew, "nnew", i32, (B,), dev),
-        _arg(block_table, "block_table", i32, (B, width), dev),
-        _arg(free_pages, "free_pages", i32, (nfree,), dev),
-        _arg(free_head, "free_head", i32, (1,), dev), B, T, width, npages, nfree,
-        _arg(slots, "slots", i32, (B, T), dev), _arg(new_lens, "new_lens", i32, (B,), dev),
-        _arg(taken, "taken", i32, (B,), dev), _arg(head, "head", i32, (1,), dev),
-        _raw_stream(dev)))
-    return out
+    slots, new_lens, taken, head = out or (None, None, None, None)
+    fn = _serving().page_map
+    if stream is None:
+        return fn(lens, nnew, block_table, free_pages, free_head, T, npages, slots, new_lens,
+                  taken, head)
+    return _on_stream(fn, stream, lens, nnew, block_table, free_pages, free_head, T, npages,
+                      slots, new_lens, taken, head)
 
 
-@_placed
 def sas_cache_append(k, v, lens, kc, vc, ksum=None, ntok=None, rows=None, slots=None,
                      inv_freq=None, interleaved: bool = False, amplitude: float = 1.0, q=None,
-                     out=None):
+                     out=None, stream=None):
     """Write new tokens' k, v [B][Hkv][T][d] into a cache, in place.
 
     The cache is kc, vc [B][Hkv][Lmax][d], or with slots [B][T] the pools
@@ -621,44 +556,17 @@ def sas_cache_append(k, v, lens, kc, vc, ksum=None, ntok=None, rows=None, slots=
     With inv_freq, k is rotated at its position first, and q [B][Hq][T][d],
     when given, beside it: returns qo (out supplies it), else None.
     """
-    B, Hkv, T, d = shape = k.shape
-    dev, dtype, i32 = k.get_device(), k.dtype, torch.int32
-    dt = _dt(k)
-    if slots is None:
-        N, npages = kc.shape[2], 0
-        cshape, sshape = (B, Hkv, N, d), (B, Hkv, N // 64, d)
-    else:
-        N, npages = 0, kc.shape[0]
-        cshape, sshape = (npages, Hkv, 64, d), (npages, Hkv, d)
-    pq = sq = po = None
-    Hq = Hkv
-    if q is not None:
-        Hq = q.shape[1]
-        qshape = (B, Hq, T, d)
-        pq, sq = _strided(q, "q", dtype, qshape, dev)
-        if out is None:
-            out = _like(q)
-        po = _arg(out, "out", dtype, qshape, dev)
-    elif out is not None:
-        raise ValueError("out goes with q")
-    pk, sk = _strided(k, "k", dtype, shape, dev)
-    pv, sv = _strided(v, "v", dtype, shape, dev)
-    half = 0 if inv_freq is None else inv_freq.numel()
-    _check("sas_cache_append", load_library().sas_cache_append(
-        pq, sq, po, pk, sk, pv, sv, dt, B, Hq, Hkv, T, d, _arg(rows, "rows", i32, (B, T), dev),
-        _arg(lens, "lens", i32, (B,), dev), _arg(ntok, "ntok", i32, (B,), dev),
-        _arg(inv_freq, "inv_freq", torch.float32, (half,), dev), 2 * half, interleaved, amplitude,
-        _arg(slots, "slots", i32, (B, T), dev), _arg(kc, "kc", dtype, cshape, dev),
-        _arg(vc, "vc", dtype, cshape, dev), N, npages,
-        None if ksum is None else _arg(ksum, "ksum", ksum.dtype, sshape, dev),
-        SAS_F32 if ksum is None else _dt(ksum), _raw_stream(dev)))
-    return out
+    fn = _serving().cache_append
+    if stream is None:
+        return fn(k, v, lens, kc, vc, ksum, ntok, rows, slots, inv_freq, interleaved, amplitude,
+                  q, out)
+    return _on_stream(fn, stream, k, v, lens, kc, vc, ksum, ntok, rows, slots, inv_freq,
+                      interleaved, amplitude, q, out)
 
 
-@_placed
 def sas_decode_tree(q, kd, vd, kc, vc, lens, ksum, topk: int, parents=None, ntok=None,
                     block_table=None, gated: int = 1, scale: float = 0.0, out=None, idx_out=None,
-                    ws=None):
+                    ws=None, stream=None):
     """Decode of a tree of drafted tokens: q [B][Hq][T][d], kd, vd [B][Hkv][T][d]
     over caches as sas_decode's (or, with block_table, sas_decode_paged's) ->
     o [B][Hq][T][d].
@@ -667,33 +575,9 @@ def sas_decode_tree(q, kd, vd, kc, vc, lens, ksum, topk: int, parents=None, ntok
     (a chain if None). ntok [B] counts the drafted tokens (all T if None); rows
     from ntok on are left as they were in out and idx_out [B][Hkv][T][topk].
     """
-    B, Hq, T, d = shape = q.shape
-    Hkv = kd.shape[1]
-    dev, dtype, i32 = q.get_device(), q.dtype, torch.int32
-    lib, dt = load_library(), _dt(q)
-    if block_table is None:
-        N, npages = kc.shape[2], 0
-        cshape, sshape = (B, Hkv, N, d), (B, Hkv, N // 64, d)
-    else:
-        N, npages = 64 * block_table.shape[1], kc.shape[0]
-        cshape, sshape = (npages, Hkv, 64, d), (npages, Hkv, d)
-    if out is None:
-        out = _like(q)
-    need = lib.sas_decode_tree_workspace_size(B, Hq, Hkv, T, N, d, topk, dt)
-    if ws is None or ws.numel() * ws.element_size() < need:
-        ws = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-    dshape = (B, Hkv, T, d)
-    _check("sas_decode_tree", lib.sas_decode_tree(
-        _arg(q, "q", dtype, shape, dev), _arg(kd, "kd", dtype, dshape, dev),
-        _arg(vd, "vd", dtype, dshape, dev), _arg(kc, "kc", dtype, cshape, dev),
-        _arg(vc, "vc", dtype, cshape, dev), dt, B, Hq, Hkv, T, N, d,
-        _arg(parents, "parents", i32, (B, T), dev), _arg(ntok, "ntok", i32, (B,), dev),
-        _arg(lens, "lens", i32, (B,), dev),
-        None if ksum is None else _arg(ksum, "ksum", ksum.dtype, sshape, dev),
-        SAS_F32 if ksum is None else _dt(ksum),
-        _arg(block_table, "block_table", i32, (B, N // 64), dev), npages, topk, gated, scale,
-        _arg(out, "out", dtype, shape, dev),
-        _arg(idx_out, "idx_out", i32, (B, Hkv, T, topk), dev) if topk else None,
-        _arg(ws, "ws", ws.dtype, ws.shape, dev), ws.numel() * ws.element_size(),
-        _raw_stream(dev)))
-    return out
+    fn = _serving().decode_tree
+    if stream is None:
+        return fn(q, kd, vd, kc, vc, lens, ksum, topk, parents, ntok, block_table, gated, scale,
+                  out, idx_out, ws)
+    return _on_stream(fn, stream, q, kd, vd, kc, vc, lens, ksum, topk, parents, ntok, block_table,
+                      gated, scale, out, idx_out, ws)
