@@ -98,7 +98,7 @@ sas_status sas_page_map(const int32_t* lens, const int32_t* nnew, int32_t* block
           "B (T + 128) must be below 2^31 (B=%d T=%d)", B, T);
   REQUIRE((long long)width * 64 < (1ll << 31), SAS_ERR_UNSUPPORTED,
           "64 width must be below 2^31 (width=%d)", width);
-  REQUIRE(B <= 65535, SAS_ERR_UNSUPPORTED, "B must be <= 65535 (got %d)", B);
+  REQUIRE(B <= 65534, SAS_ERR_UNSUPPORTED, "B must be <= 65534 (got %d)", B);
   if (B > 0) {
     REQUIRE_PTR(lens);
     REQUIRE_PTR(nnew);

@@ -24,12 +24,12 @@ constexpr int AP_THREADS = 256;
 }
 
 template <typename T, int VN, int D>
-__global__ void __launch_bounds__(AP_THREADS) k_append(AppendArgs a) {
+__global__ void __launch_bounds__(AP_THREADS, 2) k_append(AppendArgs a) {
   constexpr int U = D / (2 * VN);            // units of a row
   constexpr int RG = AP_THREADS / U;         // rows that the CTA covers at once
   constexpr int RPT = SAS_BLOCK / RG;        // rows of a thread
   static_assert(AP_THREADS % U == 0 && SAS_BLOCK % RG == 0 && RPT >= 1, "rows divide evenly");
-  __shared__ float red[RG][D];
+  __shared__ float red[2][RG][D];
   __shared__ int slot_s[SAS_BLOCK];
   __shared__ int src_s[SAS_BLOCK];
   const int b = blockIdx.z, tid = threadIdx.x;
@@ -90,71 +90,69 @@ __global__ void __launch_bounds__(AP_THREADS) k_append(AppendArgs a) {
   const bool turned = u < a.rot / (2 * VN);
   int e0, e1;
   unit_offsets<VN>(u, a.rot, a.interleaved, e0, e1);
+  if (turned) {
+    unsigned long long F[VN];
+    unit_turns<VN>(a.inv_freq, u, F);
 #pragma unroll
-  for (int i = 0; i < RPT; ++i) {
-    const int j = jb + g + i * RG;
-    if (turned && j >= 0 && j < nt) unit_sincos<VN>(a.inv_freq, u, len + j, a.amp, false, c[i], s[i]);
+    for (int i = 0; i < RPT; ++i) unit_sincos<VN>(F, len + jb + g + i * RG, a.amp, c[i], s[i]);
   }
   const int Hk = a.Hkv, Hall = Hk + (a.q ? a.Hq : 0);
   const int h0 = blockIdx.y * a.hslice, h1 = min(h0 + a.hslice, Hall);
-  for (int h = h0; h < h1; ++h) {
-    if (h >= Hk) {  // q: rotated only
-      const T* q = static_cast<const T*>(a.q) + b * a.qs[0] + (h - Hk) * a.qs[1];
-      T* y = static_cast<T*>(a.qo) + ((size_t)b * a.Hq + (h - Hk)) * a.T * D;
-#pragma unroll
-      for (int i = 0; i < RPT; ++i) {
-        const int j = jb + g + i * RG;
-        if (j < 0 || j >= nt) continue;
-        float x0[VN], x1[VN];
-        load_vec<T, VN>(q + j * a.qs[2] + e0, x0);
-        load_vec<T, VN>(q + j * a.qs[2] + e1, x1);
-        if (turned) rotate_unit<VN>(x0, x1, c[i], s[i], a.interleaved);
-        store_vec<T, VN>(y + (size_t)j * D + e0, x0);
-        store_vec<T, VN>(y + (size_t)j * D + e1, x1);
-      }
-      continue;
-    }
+  T* kc = static_cast<T*>(a.kc);
+  T* vc = static_cast<T*>(a.vc);
+  const int hk = min(h1, Hk);
+  // first element of a slot's row of head h
+  auto place = [&](int h, int slot) -> size_t {
+    return a.slots ? (((size_t)(slot >> 6) * Hk + h) * SAS_BLOCK + (slot & 63)) * D
+                   : (((size_t)b * Hk + h) * a.N + slot) * D;
+  };
+  Piece<T, VN> k0[RPT], k1[RPT], v0[RPT], v1[RPT];
+  auto load_head = [&](int h) {
     const T* k = static_cast<const T*>(a.k) + b * a.ks[0] + h * a.ks[1];
     const T* v = static_cast<const T*>(a.v) + b * a.vs[0] + h * a.vs[1];
-    // row of the cache for a slot of this head
-    auto place = [&](int slot) -> size_t {
-      return a.slots ? (((size_t)(slot >> 6) * Hk + h) * SAS_BLOCK + (slot & 63)) * D
-                     : (((size_t)b * Hk + h) * a.N + slot) * D;
-    };
-    T* kc = static_cast<T*>(a.kc);
-    T* vc = static_cast<T*>(a.vc);
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+      const int row = g + i * RG, src = src_s[row];
+      if (src >= 0) {
+        k0[i].load(k + src * a.ks[2] + e0);
+        k1[i].load(k + src * a.ks[2] + e1);
+        v0[i].load(v + src * a.vs[2] + e0);
+        v1[i].load(v + src * a.vs[2] + e1);
+      } else if (complete) {  // an older key of the block
+        const T* ko = kc + place(h, lslot - (SAS_BLOCK - 1) + row);
+        k0[i].load(ko + e0);
+        k1[i].load(ko + e1);
+      }
+    }
+  };
+  if (h0 < hk) load_head(h0);
+  for (int h = h0; h < hk; ++h) {
     float m0[VN], m1[VN];
 #pragma unroll
     for (int i = 0; i < VN; ++i) m0[i] = m1[i] = 0.f;
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
       const int row = g + i * RG;
-      const int src = src_s[row];
+      const bool fresh = src_s[row] >= 0;
+      if (!fresh && !complete) continue;
       float x0[VN], x1[VN];
-      if (src >= 0) {
-        T* ko = kc + place(slot_s[row]);
-        T* vo = vc + place(slot_s[row]);
-        float v0[VN], v1[VN];
-        load_vec<T, VN>(k + src * a.ks[2] + e0, x0);
-        load_vec<T, VN>(k + src * a.ks[2] + e1, x1);
-        load_vec<T, VN>(v + src * a.vs[2] + e0, v0);
-        load_vec<T, VN>(v + src * a.vs[2] + e1, v1);
-        if (turned) rotate_unit<VN>(x0, x1, c[i], s[i], a.interleaved);
-        store_vec<T, VN>(ko + e0, x0);
-        store_vec<T, VN>(ko + e1, x1);
-        store_vec<T, VN>(vo + e0, v0);
-        store_vec<T, VN>(vo + e1, v1);
-        if (complete) {  // the mean is that of the stored keys
-#pragma unroll
-          for (int w = 0; w < VN; ++w) {
-            m0[w] += to_f(from_f<T>(x0[w]));
-            m1[w] += to_f(from_f<T>(x1[w]));
-          }
+      if (fresh) {
+        if (turned) {
+          k0[i].unpack(x0);
+          k1[i].unpack(x1);
+          rotate_unit<VN>(x0, x1, c[i], s[i], a.interleaved);
+          k0[i].pack(x0);
+          k1[i].pack(x1);
         }
-      } else if (complete) {  // an older key of the block
-        const T* ko = kc + place(lslot - (SAS_BLOCK - 1) + row);
-        load_vec<T, VN>(ko + e0, x0);
-        load_vec<T, VN>(ko + e1, x1);
+        const size_t at = place(h, slot_s[row]);
+        k0[i].store(kc + at + e0);
+        k1[i].store(kc + at + e1);
+        v0[i].store(vc + at + e0);  // v is moved as it is
+        v1[i].store(vc + at + e1);
+      }
+      if (complete) {  // the mean is that of the stored keys
+        k0[i].unpack(x0);
+        k1[i].unpack(x1);
 #pragma unroll
         for (int w = 0; w < VN; ++w) {
           m0[w] += x0[w];
@@ -162,17 +160,19 @@ __global__ void __launch_bounds__(AP_THREADS) k_append(AppendArgs a) {
         }
       }
     }
+    if (h + 1 < hk) load_head(h + 1);  // in flight under the sum
     if (complete) {
+      float(*rs)[D] = red[(h - h0) & 1];  // two buffers: one barrier a head
 #pragma unroll
       for (int w = 0; w < VN; ++w) {
-        red[g][e0 + w] = m0[w];
-        red[g][e1 + w] = m1[w];
+        rs[g][e0 + w] = m0[w];
+        rs[g][e1 + w] = m1[w];
       }
       __syncthreads();
       if (tid < D) {
         float sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < RG; ++i) sum += red[i][tid];
+        for (int i = 0; i < RG; ++i) sum += rs[i][tid];
         sum *= 1.0f / SAS_BLOCK;
         const size_t at = a.slots ? ((size_t)(lslot >> 6) * Hk + h) * D + tid
                                   : (((size_t)b * Hk + h) * (a.N / SAS_BLOCK) + (lslot >> 6)) * D + tid;
@@ -181,7 +181,33 @@ __global__ void __launch_bounds__(AP_THREADS) k_append(AppendArgs a) {
         else
           static_cast<float*>(a.ksum)[at] = sum;
       }
-      __syncthreads();
+    }
+  }
+  // q: rotated only
+  for (int h = max(h0, Hk); h < h1; ++h) {
+    const T* q = static_cast<const T*>(a.q) + b * a.qs[0] + (h - Hk) * a.qs[1];
+    T* y = static_cast<T*>(a.qo) + ((size_t)b * a.Hq + (h - Hk)) * a.T * D;
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+      const int j = jb + g + i * RG;
+      if (j < 0 || j >= nt) continue;
+      k0[i].load(q + j * a.qs[2] + e0);
+      k1[i].load(q + j * a.qs[2] + e1);
+    }
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+      const int j = jb + g + i * RG;
+      if (j < 0 || j >= nt) continue;
+      if (turned) {
+        float x0[VN], x1[VN];
+        k0[i].unpack(x0);
+        k1[i].unpack(x1);
+        rotate_unit<VN>(x0, x1, c[i], s[i], a.interleaved);
+        k0[i].pack(x0);
+        k1[i].pack(x1);
+      }
+      k0[i].store(y + (size_t)j * D + e0);
+      k1[i].store(y + (size_t)j * D + e1);
     }
   }
 }
@@ -190,7 +216,12 @@ template <typename T, int VN, int D>
 static cudaError_t launch(AppendArgs a, cudaStream_t st) {
   const long long blocks = (a.T + SAS_BLOCK - 1) / SAS_BLOCK + 1;  // a start inside a block adds one
   const int H = a.Hkv + (a.q ? a.Hq : 0);
-  long long slices = (148 * 4 + blocks * a.B - 1) / (blocks * a.B);
+  // Heads of a CTA: all of them where the blocks fill the SMs (two prompts of
+  // 8K tokens, 8 kv heads: 29 us, against 31 with 4 heads and 34 with 1: the
+  // sines serve every head), else down to one (8 decode steps with q: 6.3 us,
+  // against 9.5 with 3 heads).
+  const long long ctas = blocks * a.B;
+  long long slices = ctas >= 148 ? 1 : (148 * 8 + ctas - 1) / ctas;
   if (slices > H) slices = H;
   a.hslice = (int)((H + slices - 1) / slices);
   dim3 grid((unsigned)blocks, (H + a.hslice - 1) / a.hslice, a.B);

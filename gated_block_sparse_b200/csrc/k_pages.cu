@@ -8,8 +8,8 @@
 // too, and its need still counts in the later sums, so every sequence finds
 // its place by a prefix sum alone, whatever happened to the others.
 //
-// Latency bounds it: a decode step moves a few kilobytes. Few tokens a
-// sequence: one CTA, a thread per sequence, one scan. Many: a grid of
+// Latency bounds it: a decode step moves a few kilobytes. Up to 16 tokens a
+// sequence: one CTA, a thread per sequence, one scan. More: a grid of
 // (sequence, 1024 tokens) CTAs that each sum the earlier needs themselves
 // (two coalesced reads of the lengths), so no CTA waits for another.
 #include "common.cuh"
@@ -77,18 +77,18 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sum_s, int* total) {
   return before + v;
 }
 
-// One CTA, one thread per sequence; with_slots = 0 leaves slots and table to
-// the grid form and only closes the step (lengths, counts, head). Every
-// length is read by the thread that later writes it, so new_lens may be lens
-// itself, and head_out free_head.
-__global__ void __launch_bounds__(PG_ROWS) k_page_rows(PageMapArgs a, int with_slots) {
-  __shared__ int ws[PG_ROWS / 32];
+// One CTA of THREADS threads, one per sequence: lengths, counts and head, and
+// with SLOTS also slots and table. Every length is read by the thread that
+// later writes it, so new_lens may be lens itself, and head_out free_head.
+template <int THREADS, bool SLOTS>
+__device__ __forceinline__ void page_rows(const PageMapArgs& a) {
+  __shared__ int ws[THREADS / 32];
   __shared__ int granted_s;
   if (threadIdx.x == 0) granted_s = 0;
   const int head = a.free_head[0];
   if (threadIdx.x == 0 && (head < 0 || head > a.nfree)) atomicOr(&g_pages_err, kErrBadIndex);
   int carry = 0;
-  for (int b0 = 0; b0 < a.B; b0 += PG_ROWS) {
+  for (int b0 = 0; b0 < a.B; b0 += THREADS) {
     const int b = b0 + (int)threadIdx.x;
     int len = 0, n = 0, have = 0, need = 0, total;
     bool ok = false;
@@ -97,12 +97,12 @@ __global__ void __launch_bounds__(PG_ROWS) k_page_rows(PageMapArgs a, int with_s
       n = a.nnew[b];
       ok = page_need(len, n, a.T, a.width, have, need);
     }
-    const int incl = block_scan<PG_ROWS / 32>(need, ws, &total);
+    const int incl = block_scan<THREADS / 32>(need, ws, &total);
     const int before = carry + incl - need;
     carry += total;
     ok = ok && page_fits(a, head, before, need);
     if (b < a.B) {
-      if (with_slots) {
+      if (SLOTS) {
         for (int j = 0; j < a.T; ++j)
           a.slots[(size_t)b * a.T + j] =
               ok && j < n ? slot_of(a, b, len, have, head + before, j) : -1;
@@ -119,9 +119,22 @@ __global__ void __launch_bounds__(PG_ROWS) k_page_rows(PageMapArgs a, int with_s
   if (threadIdx.x == 0) a.head_out[0] = head + granted_s;
 }
 
+__global__ void __launch_bounds__(PG_ROWS) k_page_rows(PageMapArgs a) {
+  page_rows<PG_ROWS, true>(a);
+}
+__global__ void __launch_bounds__(PG_ROWS) k_page_close(PageMapArgs a) {
+  page_rows<PG_ROWS, false>(a);
+}
+
+// Row b of the grid: slots and table of sequence b. Row B, where the launch
+// has one: the step's lengths, counts and head.
 __global__ void __launch_bounds__(PG_THREADS) k_page_slots(PageMapArgs a) {
   __shared__ int ws[PG_THREADS / 32];
   const int b = blockIdx.y, tid = threadIdx.x;
+  if (b == a.B) {
+    if (blockIdx.x == 0) page_rows<PG_THREADS, false>(a);
+    return;
+  }
   const int head = a.free_head[0];
   int part = 0, before, have, need;
   for (int i = tid; i < b; i += PG_THREADS) {
@@ -154,14 +167,17 @@ __global__ void __launch_bounds__(PG_THREADS) k_page_slots(PageMapArgs a) {
 
 cudaError_t launch_page_map(const PageMapArgs& a, cudaStream_t st) {
   if (a.T <= 16 || a.B == 0) {
-    k_page_rows<<<1, PG_ROWS, 0, st>>>(a, 1);
+    k_page_rows<<<1, PG_ROWS, 0, st>>>(a);
     return cudaGetLastError();
   }
+  // In place (lengths or head), the step is closed by a launch of its own,
+  // after every CTA has read them.
+  const bool in_place = a.new_lens == a.lens || a.head_out == a.free_head;
   const int per = PG_THREADS * PG_PER_THREAD;
-  k_page_slots<<<dim3((a.T + per - 1) / per, a.B), PG_THREADS, 0, st>>>(a);
+  k_page_slots<<<dim3((a.T + per - 1) / per, a.B + !in_place), PG_THREADS, 0, st>>>(a);
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  k_page_rows<<<1, PG_ROWS, 0, st>>>(a, 0);
+  if (e != cudaSuccess || !in_place) return e;
+  k_page_close<<<1, PG_ROWS, 0, st>>>(a);
   return cudaGetLastError();
 }
 

@@ -15,6 +15,7 @@ __device__ uint32_t g_rotary_err = 0;
 
 namespace {
 constexpr int RT_THREADS = 256;
+constexpr int RT_BATCH = 4;
 }
 
 // Depth of drafted token i: its number of ancestors. A parent is below its
@@ -53,23 +54,49 @@ __global__ void __launch_bounds__(RT_THREADS) k_rotary(
         (parents ? draft_depth(parents + (size_t)b * N, n, &g_rotary_err) : n);
   const bool turned = u < rot / (2 * VN);
   float c[VN], s[VN];
-  if (turned) unit_sincos<VN>(inv_freq, u, p, amp, inverse, c, s);
+  if (turned) {
+    unsigned long long F[VN];
+    unit_turns<VN>(inv_freq, u, F);
+    unit_sincos<VN>(F, p, amp, c, s);
+    if (inverse) {
+#pragma unroll
+      for (int i = 0; i < VN; ++i) s[i] = -s[i];
+    }
+  }
   int e0, e1;
   unit_offsets<VN>(u, rot, interleaved, e0, e1);
   const int h0 = blockIdx.y * hslice, h1 = min(h0 + hslice, q.H + k.H);
-#pragma unroll 4
-  for (int h = h0; h < h1; ++h) {
-    const bool isq = h < q.H;
-    const RotaryTensor& t = isq ? q : k;
-    const int hh = isq ? h : h - q.H;
-    const T* x = static_cast<const T*>(t.x) + b * t.xs[0] + hh * t.xs[1] + n * t.xs[2];
-    T* y = static_cast<T*>(t.y) + b * t.ys[0] + hh * t.ys[1] + n * t.ys[2];
-    float a[VN], bb[VN];
-    load_vec<T, VN>(x + e0, a);
-    load_vec<T, VN>(x + e1, bb);
-    if (turned) rotate_unit<VN>(a, bb, c, s, interleaved);
-    store_vec<T, VN>(y + e0, a);
-    store_vec<T, VN>(y + e1, bb);
+  // RT_BATCH heads at a time, all their loads before the first store (which may
+  // overwrite the input: in place, a thread's own elements)
+  for (int h = h0; h < h1; h += RT_BATCH) {
+    Piece<T, VN> x0[RT_BATCH], x1[RT_BATCH];
+#pragma unroll
+    for (int i = 0; i < RT_BATCH; ++i) {
+      if (h + i >= h1) break;
+      const bool isq = h + i < q.H;
+      const RotaryTensor& t = isq ? q : k;
+      const T* x = static_cast<const T*>(t.x) + b * t.xs[0] + (h + i - (isq ? 0 : q.H)) * t.xs[1] +
+                   n * t.xs[2];
+      x0[i].load(x + e0);
+      x1[i].load(x + e1);
+    }
+#pragma unroll
+    for (int i = 0; i < RT_BATCH; ++i) {
+      if (h + i >= h1) break;
+      const bool isq = h + i < q.H;
+      const RotaryTensor& t = isq ? q : k;
+      T* y = static_cast<T*>(t.y) + b * t.ys[0] + (h + i - (isq ? 0 : q.H)) * t.ys[1] + n * t.ys[2];
+      if (turned) {
+        float v0[VN], v1[VN];
+        x0[i].unpack(v0);
+        x1[i].unpack(v1);
+        rotate_unit<VN>(v0, v1, c, s, interleaved);
+        x0[i].pack(v0);
+        x1[i].pack(v1);
+      }
+      x0[i].store(y + e0);
+      x1[i].store(y + e1);
+    }
   }
 }
 
@@ -81,12 +108,15 @@ static cudaError_t launch(const RotaryTensor& q, const RotaryTensor& k, int B, i
   const long long items = (long long)N * (d / (2 * VN));
   const long long blocks = (items + RT_THREADS - 1) / RT_THREADS;
   const int H = q.H + k.H;
-  // heads per thread: as many as leave the grid about four blocks an SM
+  // Heads per thread: as many as leave the grid about four blocks an SM (small
+  // calls), but no more than two batches (q and k of 16K tokens, 40 heads: 55
+  // us with 8 heads a thread, 58 with 20; the sines of a thread are then
+  // computed five times over, beside the copies).
   const long long want = 148 * 4;
   long long slices = (want + blocks * B - 1) / (blocks * B);
-  if (slices < 1) slices = 1;
   if (slices > H) slices = H;
-  const int hslice = (int)((H + slices - 1) / slices);
+  int hslice = (int)((H + slices - 1) / slices);
+  if (hslice > 2 * RT_BATCH) hslice = 2 * RT_BATCH;
   dim3 grid((unsigned)blocks, (H + hslice - 1) / hslice, B);
   k_rotary<T, VN><<<grid, RT_THREADS, 0, st>>>(q, k, N, d, inv_freq, rot, interleaved, amp,
                                                inverse, pos, start, parents, hslice);

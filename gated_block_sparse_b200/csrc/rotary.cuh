@@ -13,8 +13,11 @@
 // 64-bit binary fraction, F = frac(f / 2 pi) 2^64: pos * F modulo 2^64 is the
 // fraction of the last turn, wrapping exactly, and the error is that of F,
 // 2^-53 f / 2 pi turns a position (2e-11 turns at 2^20 positions and f = 1).
-// The top 32 bits give the nearest quarter turn and an offset of at most an
-// eighth, whose fp32 rounding is below 3e-8 of a turn's eighth.
+// The top 32 bits give the nearest quarter turn and an offset t of at most an
+// eighth (pi/4 radians), taken in two exact parts so that only its last
+// rounding remains. There the Taylor series of sin up to t^9 and of cos up to
+// t^10 are within 2e-9 and 2e-10: eleven multiply-adds, where a general
+// sincospi would reduce its argument again.
 #pragma once
 
 #include "common.cuh"
@@ -29,35 +32,48 @@ __device__ __forceinline__ unsigned long long turns_u64(float f) {
 __device__ __forceinline__ void turn_sincos(unsigned long long F, int pos, float amp, float& c,
                                             float& s) {
   const unsigned long long ph = F * (unsigned long long)(long long)pos;
-  const uint32_t t = (uint32_t)(ph >> 32);
-  const uint32_t quarter = (t + 0x20000000u) >> 30;  // nearest quarter turn (mod 4)
-  const int off = (int)(t - (quarter << 30));        // [-2^29, 2^29): an eighth of a turn
-  float sn, cs;
-  sincospif((float)off * 4.656612873077393e-10f, &sn, &cs);  // off 2^-31 half turns
+  const uint32_t p = (uint32_t)(ph >> 32);
+  const uint32_t quarter = (p + 0x20000000u) >> 30;  // nearest quarter turn (mod 4)
+  const int off = (int)(p - (quarter << 30));        // [-2^29, 2^29): an eighth of a turn
+  // radians: off 2 pi / 2^32, the constant and off in two parts each
+  constexpr float R_HI = 1.4629180792671596e-09f;                                // 2 pi / 2^32
+  constexpr float R_LO = (float)(1.4629180792671596810513e-09 - (double)R_HI);
+  const float hi = (float)(off & ~63), lo = (float)(off & 63);
+  const float t = fmaf(hi, R_HI, fmaf(lo, R_HI, hi * R_LO)), q = t * t;
+  const float sn = fmaf(t * q, fmaf(q, fmaf(q, fmaf(q, 1.f / 362880, -1.f / 5040), 1.f / 120),
+                                    -1.f / 6), t);
+  const float cs = fmaf(q, fmaf(q, fmaf(q, fmaf(q, fmaf(q, -1.f / 3628800, 1.f / 40320),
+                                                -1.f / 720), 1.f / 24), -0.5f), 1.f);
   const float a = (quarter & 1u) ? sn : cs, b = (quarter & 1u) ? cs : sn;
   c = ((quarter == 1u || quarter == 2u) ? -a : a) * amp;
   s = ((quarter & 2u) ? -b : b) * amp;
 }
 
-// 2 VN elements of a head: VN pairs. VN = Vec16<T>::N moves 16-byte vectors,
-// VN = 1 single elements (rotated widths or strides that vectors do not fit).
-// p0 and p1 are where the two halves start: VN elements from each (half
-// layout, or an unrotated stretch), or 2 VN elements from p0 (interleaved,
-// p1 = p0 + VN).
+// A thread holds units of 2 VN elements of a head: VN pairs. VN = Vec16<T>::N
+// moves 16-byte vectors, VN = 1 single elements (rotated widths or strides that
+// vectors do not fit).
+// VN elements as they are stored. Loads are marked as read once (append, whose
+// writes the next kernel reads, gains 5% from it).
 template <typename T, int VN>
-__device__ __forceinline__ void load_vec(const T* p, float (&x)[VN]) {
-  if constexpr (VN == 1)
-    x[0] = to_f(*p);
-  else
-    Vec16<T>::load(p, x);
-}
-template <typename T, int VN>
-__device__ __forceinline__ void store_vec(T* p, const float (&x)[VN]) {
-  if constexpr (VN == 1)
-    *p = from_f<T>(x[0]);
-  else
-    Vec16<T>::store(p, x);
-}
+struct Piece {
+  uint4 v;
+  __device__ __forceinline__ void load(const T* p) { v = __ldcs(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<uint4*>(p) = v; }
+  __device__ __forceinline__ void unpack(float (&x)[VN]) const {
+    Vec16<T>::load(reinterpret_cast<const T*>(&v), x);
+  }
+  __device__ __forceinline__ void pack(const float (&x)[VN]) {
+    Vec16<T>::store(reinterpret_cast<T*>(&v), x);
+  }
+};
+template <typename T>
+struct Piece<T, 1> {
+  T v;
+  __device__ __forceinline__ void load(const T* p) { v = *p; }
+  __device__ __forceinline__ void store(T* p) const { *p = v; }
+  __device__ __forceinline__ void unpack(float (&x)[1]) const { x[0] = to_f(v); }
+  __device__ __forceinline__ void pack(const float (&x)[1]) { v = from_f<T>(x[0]); }
+};
 
 // Where unit u (2 VN elements) of a head lies: its two element offsets.
 // Units u < rot / (2 VN) are rotated, the others are passed through.
@@ -97,17 +113,19 @@ __device__ __forceinline__ void rotate_unit(float (&a)[VN], float (&b)[VN], cons
   }
 }
 
-// cos and sin of the VN pairs of rotated unit u at a position: pairs u VN ..
-// u VN + VN - 1 in both layouts.
+// Turns per position of the VN pairs of rotated unit u: pairs u VN .. u VN +
+// VN - 1 in both layouts.
 template <int VN>
-__device__ __forceinline__ void unit_sincos(const float* __restrict__ inv_freq, int u, int pos,
-                                            float amp, bool inverse, float (&c)[VN],
-                                            float (&s)[VN]) {
+__device__ __forceinline__ void unit_turns(const float* __restrict__ inv_freq, int u,
+                                           unsigned long long (&F)[VN]) {
 #pragma unroll
-  for (int i = 0; i < VN; ++i) {
-    turn_sincos(turns_u64(__ldg(inv_freq + u * VN + i)), pos, amp, c[i], s[i]);
-    if (inverse) s[i] = -s[i];
-  }
+  for (int i = 0; i < VN; ++i) F[i] = turns_u64(__ldg(inv_freq + u * VN + i));
+}
+template <int VN>
+__device__ __forceinline__ void unit_sincos(const unsigned long long (&F)[VN], int pos, float amp,
+                                            float (&c)[VN], float (&s)[VN]) {
+#pragma unroll
+  for (int i = 0; i < VN; ++i) turn_sincos(F[i], pos, amp, c[i], s[i]);
 }
 
 }  // namespace sas
