@@ -182,16 +182,34 @@ __global__ void __launch_bounds__(TA_THREADS) k_tree_attn_simt(TreeArgs a, TreeW
   }
 }
 
+// Four values through L2, zeros when !on: a predicated load, so that several go
+// out together.
+__device__ __forceinline__ float4 load_if(const float* p, bool on) {
+  float4 v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %5, 0;\n\t"
+      "mov.f32 %0, 0f00000000;\n\tmov.f32 %1, 0f00000000;\n\t"
+      "mov.f32 %2, 0f00000000;\n\tmov.f32 %3, 0f00000000;\n\t"
+      "@p ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+      : "l"(p), "r"((uint32_t)on)
+      : "memory");
+  return v;
+}
+
 // Joins the splits: o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s. One CTA
-// per 8 rows: warp w first turns row w's maxima and sums into one factor per
-// split (lane s; at most 32 splits), then thread (row, four columns) adds the
-// partial outputs, eight splits in flight. A split that saw none of a row's
-// keys has l = 0, and its partial output is not read. Eight rows side by side
-// make every access a full 32-byte sector. Latency bounds it.
+// per two rows: warps 0 and 1 turn a row's maxima and sums into one factor per
+// split (lane s; at most 32 splits); thread (row, four columns, quarter) adds
+// every fourth split's partial output, and the quarters meet in shared memory.
+// A split that saw none of a row's keys has l = 0, and its partial output is
+// not read. Two rows side by side make every access a full 32-byte sector.
+// Latency bounds it: two dependent reads.
 template <typename T, int D>
-__global__ void __launch_bounds__(256) k_tree_join(TreeArgs a, TreeWs w) {
-  constexpr int ROWS = 8, PER = D / 4;
+__global__ void __launch_bounds__(8 * D / 4) k_tree_join(TreeArgs a, TreeWs w) {
+  constexpr int ROWS = 2, PER = D / 4, QUARTERS = 4;
   __shared__ float fs[ROWS][32];
+  __shared__ float4 part[QUARTERS - 1][ROWS * PER];
   const int b = blockIdx.z, r = blockIdx.y, lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int G = a.Hq / a.Hkv, row0 = blockIdx.x * ROWS;
   const int nt = min(max(a.ntok ? __ldg(a.ntok + b) : a.T, 0), a.T);
@@ -199,35 +217,48 @@ __global__ void __launch_bounds__(256) k_tree_join(TreeArgs a, TreeWs w) {
   const int rows = G * nt;
   if (row0 >= rows) return;
   const size_t group = (size_t)b * a.Hkv + r, R = (size_t)G * a.T;
-  float2 ml = make_float2(-1e30f, 0.f);
-  if (lane < a.ns && row0 + wid < rows)
-    ml = __ldcg(w.ml + (group * a.ns + lane) * R + row0 + wid);
-  const bool seen = ml.y != 0.f;
-  const float M = warp_max(seen ? ml.x : -INFINITY);
-  const float f = seen ? exp2f(ml.x - M) : 0.f;
-  const float L = warp_sum(seen ? ml.y * f : 0.f);
-  fs[wid][lane] = seen ? f / L : -1.f;  // -1: not read
+  if (wid < ROWS) {
+    float2 ml = make_float2(-1e30f, 0.f);
+    if (lane < a.ns && row0 + wid < rows)
+      ml = __ldcg(w.ml + (group * a.ns + lane) * R + row0 + wid);
+    const bool seen = ml.y != 0.f;
+    const float M = warp_max(seen ? ml.x : -INFINITY);
+    const float f = seen ? exp2f(ml.x - M) : 0.f;
+    const float L = warp_sum(seen ? ml.y * f : 0.f);
+    fs[wid][lane] = seen ? f / L : -1.f;  // -1: not read
+  }
   __syncthreads();
-  const int i = threadIdx.x % ROWS, c4 = threadIdx.x / ROWS, row = row0 + i;
-  if (c4 >= PER || row >= rows) return;
+  const int e = threadIdx.x % (ROWS * PER), quarter = threadIdx.x / (ROWS * PER);
+  const int i = e % ROWS, c4 = e / ROWS, row = row0 + i;
   const float* src = w.part + group * a.ns * R * D + ((size_t)c4 * R + row) * 4;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s0 = 0; s0 < a.ns; s0 += 8) {
-    float4 x[8];
-    float g[8];
+  for (int s0 = quarter; s0 < a.ns; s0 += 4 * QUARTERS) {
+    float4 x[4];
+    float g[4];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      g[k] = s0 + k < a.ns ? fs[i][s0 + k] : -1.f;
-      x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (!(g[k] < 0.f)) x[k] = __ldcg(reinterpret_cast<const float4*>(src + (s0 + k) * R * D));
+    for (int k = 0; k < 4; ++k) {
+      const int s = s0 + QUARTERS * k;
+      g[k] = s < a.ns ? fs[i][s] : -1.f;
+      x[k] = load_if(src + s * R * D, !(g[k] < 0.f));
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < 4; ++k) {
       acc.x = fmaf(x[k].x, g[k], acc.x);
       acc.y = fmaf(x[k].y, g[k], acc.y);
       acc.z = fmaf(x[k].z, g[k], acc.z);
       acc.w = fmaf(x[k].w, g[k], acc.w);
     }
+  }
+  if (quarter > 0) part[quarter - 1][e] = acc;
+  __syncthreads();
+  if (quarter > 0 || row >= rows) return;
+#pragma unroll
+  for (int k = 0; k < QUARTERS - 1; ++k) {
+    const float4 y = part[k][e];
+    acc.x += y.x;
+    acc.y += y.y;
+    acc.z += y.z;
+    acc.w += y.w;
   }
   T* o = static_cast<T*>(a.o) +
          (((size_t)b * a.Hq + r * G + row / nt) * a.T + row % nt) * D + c4 * 4;
@@ -244,12 +275,12 @@ __global__ void __launch_bounds__(256) k_tree_join(TreeArgs a, TreeWs w) {
 // ------------------------------------------------------------------ host
 cudaError_t launch_tree_join(const TreeArgs& a, const TreeWs& w, int bf16, int d,
                              cudaStream_t st) {
-  const dim3 grid((a.Hq / a.Hkv * a.T + 7) / 8, a.Hkv, a.B);
+  const dim3 grid((a.Hq / a.Hkv * a.T + 1) / 2, a.Hkv, a.B);
   if (bf16)
-    return d == 128 ? tree_launch(k_tree_join<__nv_bfloat16, 128>, grid, 256, 0, st, a, w)
-                    : tree_launch(k_tree_join<__nv_bfloat16, 64>, grid, 256, 0, st, a, w);
-  return d == 128 ? tree_launch(k_tree_join<float, 128>, grid, 256, 0, st, a, w)
-                  : tree_launch(k_tree_join<float, 64>, grid, 256, 0, st, a, w);
+    return d == 128 ? tree_launch(k_tree_join<__nv_bfloat16, 128>, grid, 8 * d / 4, 0, st, a, w)
+                    : tree_launch(k_tree_join<__nv_bfloat16, 64>, grid, 8 * d / 4, 0, st, a, w);
+  return d == 128 ? tree_launch(k_tree_join<float, 128>, grid, 8 * d / 4, 0, st, a, w)
+                  : tree_launch(k_tree_join<float, 64>, grid, 8 * d / 4, 0, st, a, w);
 }
 
 template <int D>

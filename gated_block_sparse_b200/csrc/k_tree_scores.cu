@@ -77,21 +77,23 @@ template <> struct Raw8<__nv_bfloat16> {
   __device__ __forceinline__ void parts(uint4 (&out)[1]) const { out[0] = a; }
 };
 
-// CTAs an SM: the 64 fp32 values that a thread loads ahead at d = 128 need more
-// than the 128 registers of two (a spilled one would be waited for).
-template <typename S, int D>
-constexpr int scores_ctas() { return sizeof(S) * D > 256 ? 1 : 2; }
+// CTAs an SM: the 64 fp32 values that a thread loads ahead with STEP = 128 need
+// more than the 128 registers of two (a spilled one would be waited for).
+template <typename S, int STEP>
+constexpr int scores_ctas() { return sizeof(S) * STEP > 256 ? 1 : 2; }
 
 __host__ __device__ __forceinline__ int scores_cols(int T) { return (T + 15) & ~15; }
 
 }  // namespace
 
-template <typename T, typename S, int D>
-__global__ void __launch_bounds__(SC_THREADS, scores_ctas<S, D>()) k_tree_scores(TreeArgs a, TreeWs w, int stretch) {
+// STEP: columns of a tile that are in shared memory at a time (64 or D).
+template <typename T, typename S, int D, int STEP>
+__global__ void __launch_bounds__(SC_THREADS, scores_ctas<S, STEP>()) k_tree_scores(TreeArgs a, TreeWs w, int stretch) {
   constexpr int NP = sizeof(S) == 4 ? 3 : 1;     // parts of a summary
   constexpr int PC = D / 8;                      // 16-byte pieces of a bf16 row
-  constexpr int PER = SC_ROWS * PC / SC_THREADS;  // pieces of a thread
-  constexpr uint32_t A_PART = SC_ROWS * D * 2;
+  constexpr int SP = STEP / 8, PER = SC_ROWS * SP / SC_THREADS;  // pieces of a step, of a thread
+  constexpr int BI = TREE_MAX * PC / SC_THREADS;
+  constexpr uint32_t A_PART = SC_ROWS * STEP * 2;
   constexpr int VT = Vec16<T>::N;
   extern __shared__ __align__(1024) unsigned char sm[];  // parts of A, then parts of B
   __shared__ uint64_t bar;
@@ -114,32 +116,6 @@ __global__ void __launch_bounds__(SC_THREADS, scores_ctas<S, D>()) k_tree_scores
     if (tid == 0) atomicOr(err, kErrBadIndex);
     return;
   }
-  // Rows of a tile, a tile ahead; where they lie (row or page) two ahead. A row
-  // past the end reads the last one.
-  Raw8<S> x[PER];
-  int at[PER];
-  auto place_tile = [&](int m0) {
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int m = min(m0 + (tid + i * SC_THREADS) / PC, m_hi - 1);
-      at[i] = a.table ? __ldg(a.table + (size_t)b * C + m) : m;
-    }
-  };
-  auto load_tile = [&]() {
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      size_t row = group * C + at[i];
-      if (a.table) {
-        const bool ok = at[i] >= 0 && at[i] < a.npages;
-        if (!ok) atomicOr(err, kErrBadIndex);
-        row = (size_t)(ok ? at[i] : 0) * a.Hkv + r;
-      }
-      x[i].load(static_cast<const S*>(a.ksum) + row * D + (tid % PC) * 8);
-    }
-  };
-  place_tile(m_lo);
-  load_tile();
-  place_tile(m_lo + SC_ROWS);
   if (tid == 0) {
     mbar_init(&bar, 1);
     fence_mbar_init();
@@ -151,14 +127,37 @@ __global__ void __launch_bounds__(SC_THREADS, scores_ctas<S, D>()) k_tree_scores
     // wait for them and they for it.
     if (lane == 0) grid_dep_launch();
   }
-  // B: qbar in three parts, zeros behind the last token
-  const float inv_g = 1.0f / (float)G;
-#pragma unroll (NP == 3 ? 4 : 2)
-  for (int e = tid; e < NT * PC; e += SC_THREADS) {
-    const int row = e / PC, p = e % PC;
-    float s[8];
+  // Rows of a step, a step ahead; where they lie (row or page), a tile ahead. A row past the end reads the last one.
+  Raw8<S> x[PER];
+  int at[PER];
+  auto place_tile = [&](int m0) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s[i] = 0.f;
+    for (int i = 0; i < PER; ++i) {
+      const int m = min(m0 + tid / SP + i * (SC_THREADS / SP), m_hi - 1);
+      at[i] = a.table ? __ldg(a.table + (size_t)b * C + m) : m;
+    }
+  };
+  auto load_step = [&](int step) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      size_t row = group * C + at[i];
+      if (a.table) {
+        const bool ok = at[i] >= 0 && at[i] < a.npages;
+        if (!ok) atomicOr(err, kErrBadIndex);
+        row = (size_t)(ok ? at[i] : 0) * a.Hkv + r;
+      }
+      x[i].load(static_cast<const S*>(a.ksum) + row * D + step * STEP + (tid % SP) * 8);
+    }
+  };
+  place_tile(m_lo);
+  // B: qbar in three parts side by side, zeros behind the last token; its loads
+  // first, then those of the first half of A, then the parts
+  float s[BI][8];
+#pragma unroll
+  for (int e = 0; e < BI; ++e) {
+    const int row = (tid + e * SC_THREADS) / PC, p = tid % PC;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[e][i] = 0.f;
     if (row < nt) {
       const T* q = static_cast<const T*>(a.q) + (((size_t)b * a.Hq + r * G) * a.T + row) * D + p * 8;
 #pragma unroll 4
@@ -168,14 +167,22 @@ __global__ void __launch_bounds__(SC_THREADS, scores_ctas<S, D>()) k_tree_scores
           float y[VT];
           Vec16<T>::load_nc(q + (size_t)g * a.T * D + h * VT, y);
 #pragma unroll
-          for (int i = 0; i < VT; ++i) s[h * VT + i] += y[i];
+          for (int i = 0; i < VT; ++i) s[e][h * VT + i] += y[i];
         }
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s[i] *= inv_g;
     }
+  }
+  load_step(0);
+  if (D == STEP) place_tile(m_lo + SC_ROWS);
+  const float inv_g = 1.0f / (float)G;
+#pragma unroll
+  for (int e = 0; e < BI; ++e) {
+    const int row = (tid + e * SC_THREADS) / PC, p = tid % PC;
+    if (row >= NT) break;
     uint4 part[3];
-    split_bf16<3>(s, part);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[e][i] *= inv_g;
+    split_bf16<3>(s[e], part);
 #pragma unroll
     for (int k = 0; k < 3; ++k)
       *reinterpret_cast<uint4*>(sb + sw_off(k * NT + row, p, 3 * NT)) = part[k];
@@ -185,44 +192,56 @@ __global__ void __launch_bounds__(SC_THREADS, scores_ctas<S, D>()) k_tree_scores
   const uint64_t a_desc = tc::sw128_desc(smem_u32(sm), 16, 1024);
   const uint64_t b_desc = tc::sw128_desc(smem_u32(sb), 16, 1024);
   uint32_t tmem = 0;
-  int it = 0;
-  for (int m0 = m_lo; m0 < m_hi; m0 += SC_ROWS, ++it) {
-    // the previous tile's MMAs are done (waited on below), so A is free
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int e = tid + i * SC_THREADS;
-      uint4 part[NP];
-      x[i].parts(part);
-#pragma unroll
-      for (int k = 0; k < NP; ++k)
-        *reinterpret_cast<uint4*>(sm + k * A_PART + sw_off(e / PC, e % PC, SC_ROWS)) = part[k];
-    }
-    fence_proxy_async_smem();  // A and B are read by the tensor cores
-    tc::fence_before_sync();   // and the previous tile's scores have been read
-    __syncthreads();
-    tc::fence_after_sync();
-    tmem = tmem_slot;
-    if (tid == 0) {
+  uint32_t phase = 0;
+  for (int m0 = m_lo; m0 < m_hi; m0 += SC_ROWS) {
 #pragma unroll 1
-      for (int k = 0; k < NP; ++k) {
-        const uint32_t idesc = tc::idesc_bf16(128, (3 - k) * NT, 0, 0);
-        // a step along K moves a descriptor's address field (16-byte units) alone
-        const uint64_t ad = a_desc + ((k * A_PART) >> 4);
+    for (int step = 0; step < D / STEP; ++step) {
+      // the previous step's MMAs are done (waited on below), so A is free
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {  // K = D in steps of 16 (32 bytes)
-          const uint32_t c = ks >> 2, off = (ks & 3) * 32;
-          tc::mma_bf16(tmem, ad + ((c * (SC_ROWS * 128) + off) >> 4),
-                       b_desc + ((c * (uint32_t)(3 * NT) * 128 + off) >> 4), idesc,
-                       (k > 0 || ks > 0) ? 1u : 0u);
-        }
+      for (int i = 0; i < PER; ++i) {
+        uint4 part[NP];
+        x[i].parts(part);
+#pragma unroll
+        for (int k = 0; k < NP; ++k)
+          *reinterpret_cast<uint4*>(sm + k * A_PART +
+                                    sw_off(tid / SP + i * (SC_THREADS / SP), tid % SP, SC_ROWS)) =
+              part[k];
       }
-      tc::commit(&bar);
+      fence_proxy_async_smem();  // A and B are read by the tensor cores
+      tc::fence_before_sync();   // and the previous tile's scores have been read
+      __syncthreads();
+      tc::fence_after_sync();
+      tmem = tmem_slot;
+      if (tid == 0) {
+#pragma unroll 1
+        for (int k = 0; k < NP; ++k) {
+          const uint32_t idesc = tc::idesc_bf16(128, (3 - k) * NT, 0, 0);
+          // a step along K moves a descriptor's address field (16-byte units) alone
+          const uint64_t ad = a_desc + ((k * A_PART) >> 4);
+          const uint32_t chunk = (uint32_t)(3 * NT) * 128;  // 64 columns of B
+          const uint64_t bd = b_desc + ((step * (STEP / 64) * chunk) >> 4);
+#pragma unroll
+          for (int ks = 0; ks < STEP / 16; ++ks) {  // K in steps of 16 (32 bytes)
+            const uint32_t c = ks >> 2, off = (ks & 3) * 32;
+            tc::mma_bf16(tmem, ad + ((c * (SC_ROWS * 128) + off) >> 4),
+                         bd + ((c * chunk + off) >> 4), idesc,
+                         (step > 0 || k > 0 || ks > 0) ? 1u : 0u);
+          }
+        }
+        tc::commit(&bar);
+      }
+      // the next step's rows; the next tile's places once this one's are used
+      if (step + 1 < D / STEP)
+        load_step(step + 1);
+      else if (m0 + SC_ROWS < m_hi)
+        load_step(0);
+      if (step + 2 == D / STEP)
+        place_tile(m0 + SC_ROWS);
+      else if (D == STEP)
+        place_tile(m0 + 2 * SC_ROWS);
+      mbar_wait_data(&bar, phase, err);
+      phase ^= 1;
     }
-    if (m0 + SC_ROWS < m_hi) {
-      load_tile();
-      place_tile(m0 + 2 * SC_ROWS);
-    }
-    mbar_wait_data(&bar, it & 1, err);
     tc::fence_after_sync();
     // warp w: blocks 32 (w mod 4) .., tokens 32 (w / 4) ..
     const int m = m0 + 32 * (warp & 3) + lane, t0 = 32 * (warp >> 2);
@@ -256,21 +275,38 @@ __global__ void __launch_bounds__(SC_THREADS, scores_ctas<S, D>()) k_tree_scores
 }
 
 // ------------------------------------------------------------------ host
-template <typename T, typename S, int D>
-static cudaError_t launch_typed(const TreeArgs& a, const TreeWs& w, cudaStream_t st) {
+template <typename T, typename S, int D, int STEP>
+static cudaError_t launch_step(const TreeArgs& a, const TreeWs& w, cudaStream_t st) {
   const int C = a.N / SAS_BLOCK;
-  const size_t smem = (size_t)((sizeof(S) == 4 ? 3 : 1) * SC_ROWS + 3 * scores_cols(a.T)) * D * 2;
-  cudaError_t e = ensure_smem(k_tree_scores<T, S, D>, smem);
+  const size_t smem = (size_t)(sizeof(S) == 4 ? 3 : 1) * SC_ROWS * STEP * 2 +
+                      (size_t)3 * scores_cols(a.T) * D * 2;
+  cudaError_t e = ensure_smem(k_tree_scores<T, S, D, STEP>, smem);
   if (e != cudaSuccess) return e;
   // summaries of a CTA: whole tiles, and one wave of the CTAs that an SM holds
   const long long groups = (long long)a.B * a.Hkv;
-  const long long room = 148 * (smem > 112 * 1024 ? 1 : scores_ctas<S, D>());
+  const long long room = 148 * scores_ctas<S, STEP>();
   long long per_group = room / groups;
   if (per_group < 1) per_group = 1;
   long long stretch = (C + per_group - 1) / per_group;
   stretch = (stretch + SC_ROWS - 1) / SC_ROWS * SC_ROWS;
-  return tree_launch(k_tree_scores<T, S, D>, dim3((unsigned)((C + stretch - 1) / stretch), a.Hkv, a.B),
-                     SC_THREADS, smem, st, a, w, (int)stretch);
+  return tree_launch(k_tree_scores<T, S, D, STEP>,
+                     dim3((unsigned)((C + stretch - 1) / stretch), a.Hkv, a.B), SC_THREADS, smem,
+                     st, a, w, (int)stretch);
+}
+
+// Two steps of 64 columns let two CTAs of fp32 summaries at d = 128 share an SM,
+// one splitting while the other's MMAs run (512K, 64 tokens: 17 us in one step
+// of one CTA, 13 in two). Where every CTA has one tile, as in a single 64K
+// sequence, one step is shorter (the step's 23 us become 24 with two), and
+// bf16 summaries need no splitting (8 x 128K: 61 us, and 66 with two).
+template <typename T, typename S, int D>
+static cudaError_t launch_typed(const TreeArgs& a, const TreeWs& w, cudaStream_t st) {
+  if constexpr (sizeof(S) == 4 && D == 128) {
+    const long long tiles =
+        (long long)a.B * a.Hkv * ((a.N / SAS_BLOCK + SC_ROWS - 1) / SC_ROWS);
+    if (tiles > 148) return launch_step<T, S, D, 64>(a, w, st);
+  }
+  return launch_step<T, S, D, D>(a, w, st);
 }
 
 cudaError_t launch_tree_scores(const TreeArgs& a, const TreeWs& w, int bf16, int sum_bf16, int d,
