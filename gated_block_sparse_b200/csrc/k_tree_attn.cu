@@ -43,11 +43,11 @@ __global__ void __launch_bounds__(TA_THREADS) k_tree_attn_simt(TreeArgs a, TreeW
   const int split = blockIdx.x % a.ns, tile = blockIdx.x / a.ns;
   const int G = a.Hq / a.Hkv;
   const size_t group = (size_t)b * a.Hkv + r;
-  const TreeSeq s = tree_load(a, b, tree, nullptr);
-  // without selection this kernel is the call's first: it waits before it lets
-  // the next one start
+  // without selection this kernel is the call's first: it waits before anything
+  // else
   if (a.topk == 0) grid_dep_wait();
   grid_dep_launch();
+  const TreeSeq s = tree_load(a, b, tree, nullptr);
   const int rows = G * s.nt, row0 = tile * TA_ROWS;
   if (row0 >= rows) {
     grid_dep_wait();
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(8 * D / 4) k_tree_join(TreeArgs a, TreeWs w) {
   __shared__ float4 part[QUARTERS - 1][ROWS * PER];
   const int b = blockIdx.z, r = blockIdx.y, lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int G = a.Hq / a.Hkv, row0 = blockIdx.x * ROWS;
-  const int nt = min(max(a.ntok ? __ldg(a.ntok + b) : a.T, 0), a.T);
+  const int nt = min(max(a.ntok ? __ldcg(a.ntok + b) : a.T, 0), a.T);
   grid_dep_wait();
   const int rows = G * nt;
   if (row0 >= rows) return;

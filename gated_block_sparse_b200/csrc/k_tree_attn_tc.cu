@@ -178,7 +178,7 @@ __device__ __noinline__ float2 repair_row(const TreeArgs& a, const TreeWs& w, co
           if (bj == -INFINITY) continue;
         }
         float z = 0.f;
-        for (int c = 0; c < D; ++c) z = fmaf(to_f(q[c]), to_f(kp[(size_t)j * D + c]), z);
+        for (int c = 0; c < D; ++c) z = fmaf(to_f(__ldcg(q + c)), to_f(__ldcg(kp + (size_t)j * D + c)), z);
         z = (z * a.scale + bj) * LOG2E;
         if (pass == 0) {
           m = fmaxf(m, z);
@@ -188,7 +188,7 @@ __device__ __noinline__ float2 repair_row(const TreeArgs& a, const TreeWs& w, co
           if (p != 0.f)
             for (int c = 0; c < D; ++c) {
               float& x = out[tree_part_at(c, R)];
-              x = fmaf(p, to_f(vp[(size_t)j * D + c]), x);
+              x = fmaf(p, to_f(__ldcg(vp + (size_t)j * D + c)), x);
             }
         }
       }
@@ -219,11 +219,11 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
   const int split = blockIdx.x % a.ns, tile = blockIdx.x / a.ns;
   const int G = a.Hq / a.Hkv;
   const size_t group = (size_t)b * a.Hkv + r;
-  const TreeSeq s = tree_load(a, b, tree, nullptr);
-  // without selection this kernel is the call's first: it waits before it lets
-  // the next one start
+  // without selection this kernel is the call's first: it waits before anything
+  // else
   if (a.topk == 0) grid_dep_wait();
   grid_dep_launch();
+  const TreeSeq s = tree_load(a, b, tree, nullptr);
   const int rows = G * s.nt, row0 = tile * RT;
   if (row0 >= rows) {
     grid_dep_wait();

@@ -61,8 +61,8 @@ template <typename S> struct Raw8;
 template <> struct Raw8<float> {
   float4 a, b;
   __device__ __forceinline__ void load(const float* p) {
-    a = __ldg(reinterpret_cast<const float4*>(p));
-    b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    a = __ldcg(reinterpret_cast<const float4*>(p));
+    b = __ldcg(reinterpret_cast<const float4*>(p) + 1);
   }
   __device__ __forceinline__ void parts(uint4 (&out)[3]) const {
     float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
@@ -72,7 +72,7 @@ template <> struct Raw8<float> {
 template <> struct Raw8<__nv_bfloat16> {
   uint4 a;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) {
-    a = __ldg(reinterpret_cast<const uint4*>(p));
+    a = __ldcg(reinterpret_cast<const uint4*>(p));
   }
   __device__ __forceinline__ void parts(uint4 (&out)[1]) const { out[0] = a; }
 };
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(SC_THREADS, scores_ctas<S, STEP>()) k_tree_sco
   grid_dep_wait();
   for (int i = m_lo / 32 + tid; i < min((m_lo + stretch) / 32, a.words); i += SC_THREADS)
     w.ubits[group * a.words + i] = 0u;
-  const int n = __ldg(a.lens + b), ntk = a.ntok ? __ldg(a.ntok + b) : a.T;
+  const int n = __ldcg(a.lens + b), ntk = a.ntok ? __ldcg(a.ntok + b) : a.T;
   const int c0 = min(max(n, 0), a.N) / SAS_BLOCK, nt = min(max(ntk, 0), a.T);
   const int m_hi = min(m_lo + stretch, c0);
   if (m_lo >= m_hi || nt == 0) return;
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(SC_THREADS, scores_ctas<S, STEP>()) k_tree_sco
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int m = min(m0 + tid / SP + i * (SC_THREADS / SP), m_hi - 1);
-      at[i] = a.table ? __ldg(a.table + (size_t)b * C + m) : m;
+      at[i] = a.table ? __ldcg(a.table + (size_t)b * C + m) : m;
     }
   };
   auto load_step = [&](int step) {
@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(SC_THREADS, scores_ctas<S, STEP>()) k_tree_sco
 #pragma unroll
         for (int h = 0; h < 8 / VT; ++h) {
           float y[VT];
-          Vec16<T>::load_nc(q + (size_t)g * a.T * D + h * VT, y);
+          load_cg(q + (size_t)g * a.T * D + h * VT, y);
 #pragma unroll
           for (int i = 0; i < VT; ++i) s[e][h * VT + i] += y[i];
         }

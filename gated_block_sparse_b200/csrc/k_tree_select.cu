@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(SEL_THREADS) k_tree_select(TreeArgs a, TreeWs 
     for (int k = 0; k < SAS_BLOCK / GRP; ++k) {
       const int j = g + k * GRP;
       float y[VT];
-      Vec16<T>::load_nc((j < s.tail ? kc + (size_t)j * D : kd + (size_t)path[j] * D) + pc, y);
+      load_cg((j < s.tail ? kc + (size_t)j * D : kd + (size_t)path[j] * D) + pc, y);
 #pragma unroll
       for (int e = 0; e < VT; ++e) sum[e] += y[e];
     }
@@ -147,7 +147,8 @@ __global__ void __launch_bounds__(SEL_THREADS) k_tree_select(TreeArgs a, TreeWs 
       float qb = 0.f;
 #pragma unroll 4
       for (int h = 0; h < G; ++h)
-        qb += to_f(static_cast<const T*>(a.q)[(((size_t)b * a.Hq + r * G + h) * a.T + i) * D + tid]);
+        qb += to_f(__ldcg(static_cast<const T*>(a.q) +
+                          (((size_t)b * a.Hq + r * G + h) * a.T + i) * D + tid));
       float mean = 0.f;
 #pragma unroll
       for (int k = 0; k < GRP; ++k) mean += part[k * D + tid];

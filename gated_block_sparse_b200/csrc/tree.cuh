@@ -46,9 +46,9 @@ __device__ __forceinline__ int tree_depth(unsigned long long anc) { return __pop
 __device__ __forceinline__ TreeSeq tree_load(const TreeArgs& a, int b, TreeShared& t,
                                              uint32_t* err) {
   const int i = threadIdx.x;
-  const int n = __ldg(a.lens + b), nt = a.ntok ? __ldg(a.ntok + b) : a.T;
+  const int n = __ldcg(a.lens + b), nt = a.ntok ? __ldcg(a.ntok + b) : a.T;
   int p = i - 1;
-  if (a.parents && i < a.T) p = __ldg(a.parents + (size_t)b * a.T + i);
+  if (a.parents && i < a.T) p = __ldcg(a.parents + (size_t)b * a.T + i);
   TreeSeq s;
   s.n = min(max(n, 0), a.N);
   s.nt = min(max(nt, 0), a.T);
@@ -93,7 +93,7 @@ __device__ __forceinline__ unsigned long long tree_early(const TreeShared& t) {
 // Page of logical block m of sequence b (an id outside the pool is reported
 // and replaced by page 0, as in the paged decode).
 __device__ __forceinline__ int tree_page(const TreeArgs& a, int b, int m, uint32_t* err) {
-  const int p = a.table[(size_t)b * (a.N / SAS_BLOCK) + m];
+  const int p = __ldcg(a.table + (size_t)b * (a.N / SAS_BLOCK) + m);
   if (p >= 0 && p < a.npages) return p;
   if (err) atomicOr(err, kErrBadIndex);
   return 0;
@@ -150,8 +150,10 @@ struct TreeWs {
 // the one before it drains; grid_dep_wait() stands before the first access to
 // the workspace. The first kernel waits before anything else and only then
 // lets the next one start, so what the caller's earlier work wrote is complete
-// for all of them. What an earlier kernel of the call wrote is read through L2
-// (__ldcg): a line of it may still lie in an SM's L1.
+// for all of them. A kernel that starts while another runs may find old lines in
+// its SM's L1, so everything that may have changed since the last call (the
+// caller's tensors and the workspace) is read through L2: __ldcg, cp.async.cg
+// and TMA.
 template <typename... Params, typename... Args>
 inline cudaError_t tree_launch(void (*kern)(Params...), dim3 grid, int threads, size_t smem,
                                cudaStream_t st, Args... args) {
@@ -166,6 +168,13 @@ inline cudaError_t tree_launch(void (*kern)(Params...), dim3 grid, int threads, 
   c.attrs = at;
   c.numAttrs = 1;
   return cudaLaunchKernelEx(&c, kern, static_cast<Params>(args)...);
+}
+
+// A 16-byte vector through L2, as fp32 values.
+template <typename T>
+__device__ __forceinline__ void load_cg(const T* p, float* out) {
+  const uint4 v = __ldcg(reinterpret_cast<const uint4*>(p));
+  Vec16<T>::load(reinterpret_cast<const T*>(&v), out);
 }
 
 // 16 bytes from global to shared memory without a register, zeros when !full.

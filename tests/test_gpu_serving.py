@@ -634,6 +634,54 @@ def test_calls_on_another_stream_and_in_graphs():
         assert all(torch.equal(a, b) for a, b in zip(out, again))
 
 
+@pytest.mark.parametrize("topk", [0, 4])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_two_trees_at_once_and_back_to_back(dtype, topk):
+    """Calls on two streams that overlap, and calls in a row whose inputs the
+    kernel before them has just written: the same bits as one at a time."""
+    B, Hq, Hkv, d, T, N = 2, 8, 2, 128, 24, 2048
+    xs = [S.tree_case(50 + i, B, Hq, Hkv, d, T, N, [2000 - 31 * i, 700 + i], max(topk, 1), dtype,
+                      "f32", "tree") for i in range(2)]
+    sets = []
+    for x in xs:
+        t = {n: x[n + "_t"].to(DEV) for n in ("q", "kd", "vd", "kc", "vc", "ksum")}
+        t.update(lens=i32(x["lens"]), par=i32(x["parents"]))
+        sets.append(t)
+
+    def call(t, stream=None, q=None):
+        return sas.sas_decode_tree(t["q"] if q is None else q, t["kd"], t["vd"], t["kc"], t["vc"],
+                                   t["lens"], t["ksum"], topk, parents=t["par"], stream=stream)
+    want = [call(t) for t in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[call(t, s) for _ in range(30)] for t, s in zip(sets, streams) for _ in range(1)]
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert all(torch.equal(o, w) for o in g)
+    # the output of one call is the next one's query, and lengths change in place
+    chain, lens = [sets[0]["q"]], sets[0]["lens"]
+    seq = []
+    for i in range(6):
+        chain.append(call(sets[0], q=chain[-1]))
+        lens.sub_(64)
+    torch.cuda.synchronize()
+    lens.copy_(i32(xs[0]["lens"]))
+    for i in range(6):
+        torch.cuda.synchronize()
+        assert torch.equal(call(sets[0], q=chain[i]), chain[i + 1])
+        lens.sub_(64)
+        torch.cuda.synchronize()
+
+
+def test_decode_tree_defaults_are_a_full_chain():
+    x = S.tree_case(12, 2, 4, 2, 64, 9, 640, [600, 0], 3, "bf16", "f32", "chain")
+    a = tree_call(x, 3, 1, False)
+    t = {n: x[n + "_t"].to(DEV) for n in ("q", "kd", "vd", "kc", "vc", "ksum")}
+    b = sas.sas_decode_tree(t["q"], t["kd"], t["vd"], t["kc"], t["vc"], i32(x["lens"]), t["ksum"],
+                            3, ws=torch.empty(1 << 22, dtype=torch.uint8, device=DEV))
+    assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("dtype,paged", [("bf16", True), ("f32", False)])
 def test_speculative_serving_steps(dtype, paged):
     """Prompt, then rounds of draft, tree decode, acceptance, page map and
