@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(AP_THREADS, 2) k_append(AppendArgs a) {
   }
   const int off0 = len & (SAS_BLOCK - 1);
   const int jb = (int)blockIdx.x * SAS_BLOCK - off0;  // token of the block's row 0
-  if (jb >= nt) return;
+  if (jb >= (a.q ? a.T : nt)) return;  // q is rotated in all its rows
   // per row: the row of k and v that it takes (-1: none), and its place
   if (tid < SAS_BLOCK) {
     const int j = jb + tid;
@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(AP_THREADS, 2) k_append(AppendArgs a) {
   const int h0 = blockIdx.y * a.hslice, h1 = min(h0 + a.hslice, Hall);
   T* kc = static_cast<T*>(a.kc);
   T* vc = static_cast<T*>(a.vc);
-  const int hk = min(h1, Hk);
+  const int hk = jb < nt ? min(h1, Hk) : h0;
   // first element of a slot's row of head h
   auto place = [&](int h, int slot) -> size_t {
     return a.slots ? (((size_t)(slot >> 6) * Hk + h) * SAS_BLOCK + (slot & 63)) * D
@@ -190,14 +190,14 @@ __global__ void __launch_bounds__(AP_THREADS, 2) k_append(AppendArgs a) {
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
       const int j = jb + g + i * RG;
-      if (j < 0 || j >= nt) continue;
+      if (j < 0 || j >= a.T) continue;
       k0[i].load(q + j * a.qs[2] + e0);
       k1[i].load(q + j * a.qs[2] + e1);
     }
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
       const int j = jb + g + i * RG;
-      if (j < 0 || j >= nt) continue;
+      if (j < 0 || j >= a.T) continue;
       if (turned) {
         float x0[VN], x1[VN];
         k0[i].unpack(x0);

@@ -103,7 +103,7 @@ sas_status sas_page_map(const int32_t* lens, const int32_t* nnew, int32_t* block
  *   [npages][Hkv][d], of type sum_dt (as sas_block_summary computes it; a
  *   block with a token left out keeps its summary);
  *   q [B][Hq][T][d], when given, is rotated at the same positions into
- *   qo [B][Hq][T][d] (contiguous), rows from ntok[b] on left as they were.
+ *   qo [B][Hq][T][d] (contiguous), all its rows.
  *   k, v [B][Hkv][T][d] and q are read through element strides {batch, head,
  *     token} (host memory, NULL = contiguous), as in sas_rotary
  *   lens [B], the lengths before; ntok [B] or NULL (T everywhere); rows [B][T]

@@ -319,10 +319,7 @@ def test_cache_append_matches_the_oracle(c):
         pos = np.asarray(lens)[:, None] + np.arange(T)
         ref = SO.rotate(x["q64"], pos, f64, inter, amp)
         tol = rot_tol(x["q64"], ref, rot, inter, amp, dtype)
-        for b in range(B):
-            n = ntok[b]
-            assert (np.abs(np64(qo)[b, :, :n] - ref[b, :, :n]) <= tol[b, :, :n]).all()
-            assert (qo[b, :, n:] == 7.0).all()
+        assert (np.abs(np64(qo) - ref) <= tol).all()  # rows past ntok too
 
 
 def test_cache_append_leaves_out_what_is_out_of_range():
