@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(TA_THREADS) k_tree_attn_simt(TreeArgs a, TreeW
     }
     cp_async_wait();
     __syncthreads();
-    float z[TA_WROWS][2];
+    float z[TA_WROWS][2], p[TA_WROWS][2];
 #pragma unroll
     for (int i = 0; i < TA_WROWS; ++i) z[i][0] = z[i][1] = 0.f;
 #pragma unroll 4
@@ -147,19 +147,31 @@ __global__ void __launch_bounds__(TA_THREADS) k_tree_attn_simt(TreeArgs a, TreeW
       const float z0 = bias[0] == -INFINITY ? -INFINITY : fmaf(z[i][0], c1, bias[0]);
       const float z1 = bias[1] == -INFINITY ? -INFINITY : fmaf(z[i][1], c1, bias[1]);
       const float mx = warp_max(fmaxf(z0, z1));
+      p[i][0] = p[i][1] = 0.f;
       if (!(mx > -INFINITY) && !__any_sync(0xffffffffu, z0 != z0 || z1 != z1)) continue;
       const float mn = fmaxf(m[i], mx), alpha = exp2f(m[i] - mn);
-      const float p0 = exp2f(z0 - mn), p1 = exp2f(z1 - mn);
+      p[i][0] = exp2f(z0 - mn);
+      p[i][1] = exp2f(z1 - mn);
       m[i] = mn;
-      l[i] = l[i] * alpha + warp_sum(p0 + p1);
+      l[i] = l[i] * alpha + warp_sum(p[i][0] + p[i][1]);
 #pragma unroll
       for (int e = 0; e < E; ++e) acc[i][e] *= alpha;
-#pragma unroll 4
-      for (int j = 0; j < SAS_BLOCK; ++j) {
-        const float p = __shfl_sync(0xffffffffu, j < 32 ? p0 : p1, j & 31);
-        if (p != 0.f) {  // a masked key's value is not touched
+    }
+    // O += P V: a key's values are read once for the warp's rows
 #pragma unroll
-          for (int e = 0; e < E; ++e) acc[i][e] = fmaf(p, vs[j * D + lane * E + e], acc[i][e]);
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll 4
+      for (int j = 0; j < 32; ++j) {
+        float v[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = vs[(32 * h + j) * D + lane * E + e];
+#pragma unroll
+        for (int i = 0; i < TA_WROWS; ++i) {
+          const float pj = __shfl_sync(0xffffffffu, p[i][h], j);
+          if (pj != 0.f) {  // a masked key's value is not touched
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[i][e] = fmaf(pj, v[e], acc[i][e]);
+          }
         }
       }
     }
@@ -199,17 +211,17 @@ __device__ __forceinline__ float4 load_if(const float* p, bool on) {
 }
 
 // Joins the splits: o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s. One CTA
-// per two rows: warps 0 and 1 turn a row's maxima and sums into one factor per
-// split (lane s; at most 32 splits); thread (row, four columns, quarter) adds
-// every fourth split's partial output, and the quarters meet in shared memory.
-// A split that saw none of a row's keys has l = 0, and its partial output is
-// not read. Two rows side by side make every access a full 32-byte sector.
-// Latency bounds it: two dependent reads.
-template <typename T, int D>
+// per 8 / PARTS rows: a warp turns a row's maxima and sums into one factor per
+// split (lane s; at most 32 splits); thread (row, four columns, part) adds every
+// PARTS-th split's partial output, four in flight, and the parts meet in shared
+// memory. A split that saw none of a row's keys has l = 0, and its partial
+// output is not read. Two rows or more side by side make every access a full
+// 32-byte sector. Latency bounds it: two dependent reads.
+template <typename T, int D, int PARTS>
 __global__ void __launch_bounds__(8 * D / 4) k_tree_join(TreeArgs a, TreeWs w) {
-  constexpr int ROWS = 2, PER = D / 4, QUARTERS = 4;
+  constexpr int ROWS = 8 / PARTS, PER = D / 4, WARPS = 8 * PER / 32;
   __shared__ float fs[ROWS][32];
-  __shared__ float4 part[QUARTERS - 1][ROWS * PER];
+  __shared__ float4 part[PARTS > 1 ? PARTS - 1 : 1][ROWS * PER];
   const int b = blockIdx.z, r = blockIdx.y, lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int G = a.Hq / a.Hkv, row0 = blockIdx.x * ROWS;
   const int nt = min(max(a.ntok ? __ldcg(a.ntok + b) : a.T, 0), a.T);
@@ -217,27 +229,26 @@ __global__ void __launch_bounds__(8 * D / 4) k_tree_join(TreeArgs a, TreeWs w) {
   const int rows = G * nt;
   if (row0 >= rows) return;
   const size_t group = (size_t)b * a.Hkv + r, R = (size_t)G * a.T;
-  if (wid < ROWS) {
+  for (int i = wid; i < ROWS; i += WARPS) {
     float2 ml = make_float2(-1e30f, 0.f);
-    if (lane < a.ns && row0 + wid < rows)
-      ml = __ldcg(w.ml + (group * a.ns + lane) * R + row0 + wid);
+    if (lane < a.ns && row0 + i < rows) ml = __ldcg(w.ml + (group * a.ns + lane) * R + row0 + i);
     const bool seen = ml.y != 0.f;
     const float M = warp_max(seen ? ml.x : -INFINITY);
     const float f = seen ? exp2f(ml.x - M) : 0.f;
     const float L = warp_sum(seen ? ml.y * f : 0.f);
-    fs[wid][lane] = seen ? f / L : -1.f;  // -1: not read
+    fs[i][lane] = seen ? f / L : -1.f;  // -1: not read
   }
   __syncthreads();
-  const int e = threadIdx.x % (ROWS * PER), quarter = threadIdx.x / (ROWS * PER);
+  const int e = threadIdx.x % (ROWS * PER), p = threadIdx.x / (ROWS * PER);
   const int i = e % ROWS, c4 = e / ROWS, row = row0 + i;
   const float* src = w.part + group * a.ns * R * D + ((size_t)c4 * R + row) * 4;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s0 = quarter; s0 < a.ns; s0 += 4 * QUARTERS) {
+  for (int s0 = p; s0 < a.ns; s0 += 4 * PARTS) {
     float4 x[4];
     float g[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int s = s0 + QUARTERS * k;
+      const int s = s0 + PARTS * k;
       g[k] = s < a.ns ? fs[i][s] : -1.f;
       x[k] = load_if(src + s * R * D, !(g[k] < 0.f));
     }
@@ -249,17 +260,20 @@ __global__ void __launch_bounds__(8 * D / 4) k_tree_join(TreeArgs a, TreeWs w) {
       acc.w = fmaf(x[k].w, g[k], acc.w);
     }
   }
-  if (quarter > 0) part[quarter - 1][e] = acc;
-  __syncthreads();
-  if (quarter > 0 || row >= rows) return;
+  if constexpr (PARTS > 1) {
+    if (p > 0) part[p - 1][e] = acc;
+    __syncthreads();
+    if (p > 0) return;
 #pragma unroll
-  for (int k = 0; k < QUARTERS - 1; ++k) {
-    const float4 y = part[k][e];
-    acc.x += y.x;
-    acc.y += y.y;
-    acc.z += y.z;
-    acc.w += y.w;
+    for (int k = 0; k < PARTS - 1; ++k) {
+      const float4 y = part[k][e];
+      acc.x += y.x;
+      acc.y += y.y;
+      acc.z += y.z;
+      acc.w += y.w;
+    }
   }
+  if (row >= rows) return;
   T* o = static_cast<T*>(a.o) +
          (((size_t)b * a.Hq + r * G + row / nt) * a.T + row % nt) * D + c4 * 4;
   if constexpr (sizeof(T) == 2) {
@@ -273,14 +287,22 @@ __global__ void __launch_bounds__(8 * D / 4) k_tree_join(TreeArgs a, TreeWs w) {
 }
 
 // ------------------------------------------------------------------ host
+// Parts of a row's splits: four where there are many splits, which then means
+// few rows; one thread adds up to eight.
+template <typename T, int D>
+static cudaError_t launch_join(const TreeArgs& a, const TreeWs& w, cudaStream_t st) {
+  const int rows = a.Hq / a.Hkv * a.T;
+  if (a.ns > 8)
+    return tree_launch(k_tree_join<T, D, 4>, dim3((rows + 1) / 2, a.Hkv, a.B), 8 * D / 4, 0, st, a, w);
+  return tree_launch(k_tree_join<T, D, 1>, dim3((rows + 7) / 8, a.Hkv, a.B), 8 * D / 4, 0, st, a, w);
+}
+
 cudaError_t launch_tree_join(const TreeArgs& a, const TreeWs& w, int bf16, int d,
                              cudaStream_t st) {
-  const dim3 grid((a.Hq / a.Hkv * a.T + 1) / 2, a.Hkv, a.B);
   if (bf16)
-    return d == 128 ? tree_launch(k_tree_join<__nv_bfloat16, 128>, grid, 8 * d / 4, 0, st, a, w)
-                    : tree_launch(k_tree_join<__nv_bfloat16, 64>, grid, 8 * d / 4, 0, st, a, w);
-  return d == 128 ? tree_launch(k_tree_join<float, 128>, grid, 8 * d / 4, 0, st, a, w)
-                  : tree_launch(k_tree_join<float, 64>, grid, 8 * d / 4, 0, st, a, w);
+    return d == 128 ? launch_join<__nv_bfloat16, 128>(a, w, st)
+                    : launch_join<__nv_bfloat16, 64>(a, w, st);
+  return d == 128 ? launch_join<float, 128>(a, w, st) : launch_join<float, 64>(a, w, st);
 }
 
 template <int D>
@@ -300,7 +322,8 @@ cudaError_t launch_tree_attn_simt(const TreeArgs& a, const TreeWs& w, int d, cud
 
 // Splits of a kv group's units: as many as one wave of two CTAs an SM holds (a
 // second, shorter wave would cost another start), no more than the units that
-// the tokens can select, and at most one per lane of the join.
+// the tokens can select, and at most one per lane of the join. Even two units
+// are split: a unit of one CTA costs as much as the join.
 int tree_splits(int B, int Hq, int Hkv, int T, int N, int topk, int bf16) {
   const int tile = bf16 ? 128 : TA_ROWS;
   const long long tiles = ((long long)(Hq / Hkv) * T + tile - 1) / tile;

@@ -19,20 +19,18 @@ namespace sas {
 __device__ uint32_t g_tree_select_err = 0;
 
 namespace {
-constexpr int SEL_THREADS = 256;
-constexpr int SEL_WARPS = SEL_THREADS / 32;
-constexpr int SEL_BUCKETS = SEL_THREADS;  // one a thread
 constexpr int SEL_LIST = 512;  // candidates ranked by counting
 constexpr float LOG2E = 1.4426950408889634f;
 }  // namespace
 
+template <int THREADS>
 __device__ __forceinline__ float block_sum(float v, float* red) {
   v = warp_sum(v);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
   float t = 0.f;
 #pragma unroll
-  for (int i = 0; i < SEL_WARPS; ++i) t += red[i];
+  for (int i = 0; i < THREADS / 32; ++i) t += red[i];
   __syncthreads();
   return t;
 }
@@ -41,6 +39,7 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
 // sets with more equal or near-equal keys than the list holds: the threshold
 // bit by bit, then the keys equal to it in block order. Every thread owns the
 // stretch [lo, hi). Returns through th and last (shared).
+template <int THREADS>
 __device__ __noinline__ void select_by_bits(const uint32_t* keys, int lo, int hi, int kk,
                                             uint32_t* scan, uint32_t* th_s, int* last_s) {
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
@@ -54,7 +53,7 @@ __device__ __noinline__ void select_by_bits(const uint32_t* keys, int lo, int hi
     __syncthreads();
     c = 0;
 #pragma unroll
-    for (int i = 0; i < SEL_WARPS; ++i) c += scan[i];
+    for (int i = 0; i < THREADS / 32; ++i) c += scan[i];
     if (c >= (uint32_t)kk) th = cand;
     __syncthreads();
   }
@@ -73,7 +72,7 @@ __device__ __noinline__ void select_by_bits(const uint32_t* keys, int lo, int hi
   __syncthreads();
   uint32_t before = v - ((above << 16) | equal), all = 0;
 #pragma unroll
-  for (int i = 0; i < SEL_WARPS; ++i) {
+  for (int i = 0; i < THREADS / 32; ++i) {
     before += i < wid ? scan[i] : 0u;
     all += scan[i];
   }
@@ -85,13 +84,14 @@ __device__ __noinline__ void select_by_bits(const uint32_t* keys, int lo, int hi
   __syncthreads();
 }
 
-template <typename T, typename S, int D>
-__global__ void __launch_bounds__(SEL_THREADS) k_tree_select(TreeArgs a, TreeWs w) {
+template <typename T, typename S, int D, int THREADS>
+__global__ void __launch_bounds__(THREADS) k_tree_select(TreeArgs a, TreeWs w) {
+  constexpr int SEL_WARPS = THREADS / 32, SEL_BUCKETS = THREADS;  // a bucket a thread
   extern __shared__ __align__(16) float vals[];  // C_i scores
   __shared__ TreeShared tree;
   __shared__ float red[SEL_WARPS];
   __shared__ uint32_t scan[SEL_WARPS];
-  __shared__ float part[SEL_THREADS * 8];  // at most 8 columns of a key a thread
+  __shared__ float part[THREADS * 8];  // at most 8 columns of a key a thread
   __shared__ int path[SAS_BLOCK];
   __shared__ float red2[SEL_WARPS];
   __shared__ int hist[SEL_BUCKETS];
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(SEL_THREADS) k_tree_select(TreeArgs a, TreeWs 
     // Mean key of the tail's block as this path fills it: the tail's keys, then
     // the path's first ones. Thread (group, piece) sums every GRP-th key of one
     // 16-byte piece, all its loads in flight; the groups meet in shared memory.
-    constexpr int VT = Vec16<T>::N, PIECES = D / VT, GRP = SEL_THREADS / PIECES;
+    constexpr int VT = Vec16<T>::N, PIECES = D / VT, GRP = THREADS / PIECES;
     const int pc = (tid % PIECES) * VT, g = tid / PIECES;
     if (tid < TREE_MAX && (anc >> tid & 1ull)) {
       const int at = s.tail + __popcll(anc & ((1ull << tid) - 1ull));
@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(SEL_THREADS) k_tree_select(TreeArgs a, TreeWs 
       mean = to_f(from_f<S>(mean * (1.0f / SAS_BLOCK)));
       dot = qb * (1.0f / (float)G) * mean;
     }
-    virt = block_sum(dot, red) * a.scale;
+    virt = block_sum<THREADS>(dot, red) * a.scale;
   }
   if (tid == 0) {
     cnt_s = 0;
@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(SEL_THREADS) k_tree_select(TreeArgs a, TreeWs 
   const float* sc = w.scores + row * tree_stride(C);
   float mx = -INFINITY;
 #pragma unroll 4
-  for (int m = 4 * tid; m < s.c0; m += 4 * SEL_THREADS) {
+  for (int m = 4 * tid; m < s.c0; m += 4 * THREADS) {
     float4 v = __ldcg(reinterpret_cast<const float4*>(sc + m));
     if (m + 1 >= s.c0) v.y = -INFINITY;
     if (m + 2 >= s.c0) v.z = -INFINITY;
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(SEL_THREADS) k_tree_select(TreeArgs a, TreeWs 
   const float bound = bucket_s > 0 ? (float)bucket_s : -INFINITY;
   // The sum of the gate's softmax, and the list of the keys at or above the bound.
   float sum = 0.f;
-  for (int m0 = 0; m0 < Ci; m0 += 4 * SEL_THREADS) {
+  for (int m0 = 0; m0 < Ci; m0 += 4 * THREADS) {
     const int m = m0 + 4 * tid;
     float v[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
     if (m + 4 <= Ci) {
@@ -275,11 +275,11 @@ __global__ void __launch_bounds__(SEL_THREADS) k_tree_select(TreeArgs a, TreeWs 
       }
     }
   }
-  const float lse = mx + logf(block_sum(sum, red));  // its barriers also close the list
+  const float lse = mx + logf(block_sum<THREADS>(sum, red));  // its barriers also close the list
   const int n = cnt_s;
   if (kk > 0 && n <= SEL_LIST) {
     // unique keys: a candidate's rank is the number of larger ones
-    for (int e = tid; e < n; e += SEL_THREADS) {
+    for (int e = tid; e < n; e += THREADS) {
       const unsigned long long key = list[e];
       const int rank = count_above(list, n, key);
       if (rank < kk) {
@@ -304,12 +304,12 @@ __global__ void __launch_bounds__(SEL_THREADS) k_tree_select(TreeArgs a, TreeWs 
       a.idx_out[row * a.topk + at] = m;
     }
   } else if (kk > 0) {
-    const int per = ((Ci + SEL_THREADS - 1) / SEL_THREADS) | 1;  // odd: no bank conflicts
+    const int per = ((Ci + THREADS - 1) / THREADS) | 1;  // odd: no bank conflicts
     const int lo = min(tid * per, Ci), hi = min(lo + per, Ci);
     uint32_t* keys = reinterpret_cast<uint32_t*>(vals);
-    for (int m = tid; m < Ci; m += SEL_THREADS) keys[m] = score_key(vals[m]);
+    for (int m = tid; m < Ci; m += THREADS) keys[m] = score_key(vals[m]);
     __syncthreads();
-    select_by_bits(keys, lo, hi, kk, scan, &th_s, &last_s);
+    select_by_bits<THREADS>(keys, lo, hi, kk, scan, &th_s, &last_s);
     const uint32_t th = th_s;
     const int last = last_s;
     // places by counting the kept blocks of the earlier threads
@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(SEL_THREADS) k_tree_select(TreeArgs a, TreeWs 
       }
   }
   if (a.idx_out)
-    for (int p = kk + tid; p < a.topk; p += SEL_THREADS) a.idx_out[row * a.topk + p] = -1;
+    for (int p = kk + tid; p < a.topk; p += THREADS) a.idx_out[row * a.topk + p] = -1;
   if (tid == 0) {
     TreeRow t;
     t.lse = lse;
@@ -346,12 +346,21 @@ __global__ void __launch_bounds__(SEL_THREADS) k_tree_select(TreeArgs a, TreeWs 
 }
 
 // ------------------------------------------------------------------ host
+template <typename T, typename S, int D, int THREADS>
+static cudaError_t launch_threads(const TreeArgs& a, const TreeWs& w, cudaStream_t st) {
+  const size_t smem = (size_t)(tree_stride(a.N / SAS_BLOCK) + 4) * sizeof(float);
+  cudaError_t e = ensure_smem(k_tree_select<T, S, D, THREADS>, smem);
+  if (e != cudaSuccess) return e;
+  return tree_launch(k_tree_select<T, S, D, THREADS>, dim3(a.T, a.Hkv, a.B), THREADS, smem, st, a, w);
+}
+
+// Threads of a row: 128 up to 256 blocks, where the rows that fit an SM count for
+// more than each row's time (four sequences of 120 tokens, 32 drafted: 25 us a
+// call, 30 with 256); 256 beyond.
 template <typename T, typename S, int D>
 static cudaError_t launch_typed(const TreeArgs& a, const TreeWs& w, cudaStream_t st) {
-  const size_t smem = (size_t)(tree_stride(a.N / SAS_BLOCK) + 4) * sizeof(float);
-  cudaError_t e = ensure_smem(k_tree_select<T, S, D>, smem);
-  if (e != cudaSuccess) return e;
-  return tree_launch(k_tree_select<T, S, D>, dim3(a.T, a.Hkv, a.B), SEL_THREADS, smem, st, a, w);
+  return a.N / SAS_BLOCK <= 256 ? launch_threads<T, S, D, 128>(a, w, st)
+                                 : launch_threads<T, S, D, 256>(a, w, st);
 }
 
 cudaError_t launch_tree_select(const TreeArgs& a, const TreeWs& w, int bf16, int sum_bf16, int d,

@@ -368,6 +368,11 @@ TREE = [  # dtype, sums, B, Hq, Hkv, d, T, N, lens, ntok, topk, gated, kind, pag
     ("bf16", "f32", 1, 2, 2, 128, 1, 640, [640], None, 3, 1, "chain", False),
     ("bf16", "f32", 2, 2, 1, 64, 64, 128, [1, 127], None, 0, 1, "chain", True),
     ("bf16", "f32", 1, 7, 1, 128, 50, 8192, [8100], None, 40, 1, "tree", False),
+    # short caches: one, two and four copies of the rows
+    ("bf16", "bf16", 2, 8, 1, 128, 33, 128, [127, 40], [33, 20], 2, 1, "tree", True),
+    ("bf16", "f32", 3, 4, 1, 64, 13, 128, [64, 128, 0], [13, 2, 7], 5, 1, "chain", False),
+    ("bf16", "f32", 1, 2, 2, 128, 9, 512, [480], None, 0, 1, "tree", False),
+    ("f32", "f32", 2, 6, 2, 128, 9, 128, [100, 1], None, 1, 1, "tree", False),
 ]
 
 
