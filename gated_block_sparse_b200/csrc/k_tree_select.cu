@@ -6,7 +6,13 @@
 //   scores that block, s_i,c0 = scale qbar_i . mean of its 64 keys (rounded to
 //   the summaries' type).
 //
-// k_tree_select: one CTA per row.
+// k_tree_select: one CTA per row. The row's scores go into shared memory once;
+// the threads' maxima bound the topk-th score, the few scores above the bound
+// are ranked by counting, and the gate's sum is taken on the way. What it leaves
+// is one 16-byte record a row and one bit a block: the attention reads a row's
+// score of a block and the record, and no list is searched or sorted. Latency
+// bounds it (64K, 4 tokens: 3 us behind the scores; 512K, 64 tokens, 512 rows of
+// 8191 scores: 9 us).
 #include <math.h>
 
 #include "common.cuh"
