@@ -594,6 +594,33 @@ def test_binding_refuses_other_types_shapes_and_layouts():
         sas.sas_decode_tree(q, q[:, :, :3], q, q, q, i, None, 0)
 
 
+def test_outputs_of_a_call_are_ordinary_tensors():
+    """Outputs carved from one allocation: contiguous, aligned, apart, usable by
+    torch, and any of them may be supplied instead."""
+    q, k = torch.randn(1, 3, 5, 64, device=DEV), torch.randn(1, 1, 5, 64, device=DEV)
+    f = rope.inv_freq(64)[0].to(DEV)
+    qo, ko = sas.sas_rotary(q, f, k=k)
+    assert qo.is_contiguous() and ko.is_contiguous() and ko.data_ptr() % 16 == 0
+    assert qo.shape == q.shape and ko.shape == k.shape
+    mine = torch.empty_like(k)
+    q2, k2 = sas.sas_rotary(q, f, k=k, out=(None, mine))
+    assert k2 is mine and torch.equal(q2, qo) and torch.equal(k2, ko)
+    keep = qo.clone()
+    ko.zero_()
+    assert torch.equal(qo, keep) and torch.equal(qo.transpose(1, 2).reshape(-1), keep.transpose(1, 2).reshape(-1))
+    del qo
+    torch.cuda.empty_cache()
+    assert (ko + 1 == 1).all()
+    lens = i32([3, 0, 70])
+    new = torch.empty_like(lens)
+    out = sas.sas_page_map(lens, i32([1, 0, 2]), i32(np.arange(6).reshape(3, 2)), i32([7, 8]), i32([0]),
+                           3, 9, out=(None, new, None, None))
+    assert out[1] is new and new.tolist() == [4, 0, 72]
+    assert all(t.is_contiguous() and t.data_ptr() % 16 == 0 for t in out)
+    assert [tuple(t.shape) for t in out] == [(3, 3), (3,), (3,), (1,)]
+    assert out[0].tolist() == [[3, -1, -1], [-1] * 3, [5 * 64 + 6, 5 * 64 + 7, -1]]
+
+
 # ------------------------------------------------------------ streams, graphs
 def test_calls_on_another_stream_and_in_graphs():
     B, Hq, Hkv, d, T, N, topk = 2, 4, 2, 128, 6, 1024, 4
