@@ -47,7 +47,8 @@ __global__ void __launch_bounds__(TA_THREADS) k_tree_attn_simt(TreeArgs a, TreeW
   // else
   if (a.topk == 0) grid_dep_wait();
   grid_dep_launch();
-  const TreeSeq s = tree_load(a, b, tree, nullptr);
+  const bool report = a.topk == 0 && blockIdx.x == 0 && r == 0;  // else the selection does
+  const TreeSeq s = tree_load(a, b, tree, report ? &g_tree_attn_err : nullptr);
   const int rows = G * s.nt, row0 = tile * TA_ROWS;
   if (row0 >= rows) {
     grid_dep_wait();

@@ -228,7 +228,8 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
   // else
   if (a.topk == 0) grid_dep_wait();
   grid_dep_launch();
-  const TreeSeq s = tree_load(a, b, tree, nullptr);
+  const bool report = a.topk == 0 && blockIdx.x == 0 && r == 0;  // else the selection does
+  const TreeSeq s = tree_load(a, b, tree, report ? &g_tree_tc_err : nullptr);
   const int rows = G * s.nt, row0 = tile * RT;
   if (row0 >= rows) {
     grid_dep_wait();

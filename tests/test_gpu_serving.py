@@ -564,6 +564,13 @@ def test_decode_tree_reports_bad_parents_pages_and_lengths():
         x["lens"], x["ntok"] = np.array(lens), np.array(ntok)
         tree_call(x, topk, 1, False)
         assert sas.sas_device_status(clear=True)[0] == 5
+    for dtype in ("bf16", "f32"):  # without a selection too
+        x = S.tree_case(6, B, Hq, Hkv, d, T, N, [513], 1, dtype, "f32", "chain")
+        tree_call(x, 0, 1, False)
+        assert sas.sas_device_status(clear=True)[0] == 5
+        x["lens"], x["parents"] = np.array([400]), par + 2
+        tree_call(x, 0, 1, False)
+        assert sas.sas_device_status(clear=True)[0] == 5
 
 
 def test_binding_refuses_other_types_shapes_and_layouts():
@@ -700,6 +707,48 @@ def test_two_trees_at_once_and_back_to_back(dtype, topk):
         assert torch.equal(call(sets[0], q=chain[i]), chain[i + 1])
         lens.sub_(64)
         torch.cuda.synchronize()
+
+
+def test_caches_past_two_billion_elements():
+    """Three sequences of 2^20 - 40 tokens, 8 kv heads of 128: element offsets
+    pass 2^31. The last sequence against a call on a copy of its own (other
+    splits: the tree's bound twice), and tokens written at its end."""
+    B, Hq, Hkv, d, T, N, topk = 3, 8, 8, 128, 4, 1 << 20, 2
+    g = torch.Generator(device=DEV).manual_seed(1)
+    kc = torch.zeros((B, Hkv, N, d), dtype=torch.bfloat16, device=DEV)
+    vc = torch.zeros_like(kc)
+    assert kc.numel() > 1 << 31
+    ks = torch.zeros((B, Hkv, N // 64, d), device=DEV)
+    n = N - 40
+    q = torch.randn((B, Hq, T, d), generator=g, device=DEV).bfloat16()
+    kd = torch.randn((B, Hkv, T, d), generator=g, device=DEV).bfloat16()
+    vd = torch.randn((B, Hkv, T, d), generator=g, device=DEV).bfloat16()
+    for m in (5, N // 64 - 3):  # two blocks that score, and the tail
+        kc[:, :, 64 * m:64 * m + 64] = torch.randn((B, Hkv, 64, d), generator=g, device=DEV).bfloat16()
+        vc[:, :, 64 * m:64 * m + 64] = torch.randn((B, Hkv, 64, d), generator=g, device=DEV).bfloat16()
+        ks[:, :, m] = 3.0 * q[:, :, 0].float()
+    vc[:, :, N - 64:n] = 1.0
+    lens = i32([n] * B)
+    idx = torch.empty((B, Hkv, T, topk), dtype=torch.int32, device=DEV)
+    o = sas.sas_decode_tree(q, kd, vd, kc, vc, lens, ks, topk, idx_out=idx)
+    own = [t[2:].clone() for t in (q, kd, vd, kc, vc, ks)]
+    one = sas.sas_decode_tree(own[0], own[1], own[2], own[3], own[4], lens[2:].clone(), own[5], topk)
+    assert (idx[:, :, 0] == torch.tensor([5, N // 64 - 3], device=DEV)).all()
+    err = (o[2:].float() - one.float()).abs().max()
+    # weights and outputs round to bf16 on both sides; |v| < 5.5
+    assert err <= 2 * 2 * 2.0 ** -8 * 5.5
+    table = torch.arange(B * N // 64, dtype=torch.int32, device=DEV).view(B, -1)
+    pools = [t.view(B, Hkv, N // 64, 64, d)[2:].transpose(1, 2).reshape(-1, Hkv, 64, d).contiguous()
+             for t in (kc, vc)]
+    sas.sas_cache_append(kd, vd, lens, kc, vc, ksum=ks)
+    assert torch.equal(kc[2, :, n:n + T], kd[2]) and torch.equal(vc[2, :, n:n + T], vd[2])
+    assert (kc[:, :, n + T:] == 0).all() and (kc[0, :, N - 64:n] == 0).all()
+    paged = sas.sas_decode_tree(own[0], own[1], own[2], pools[0], pools[1], lens[2:].clone(),
+                                own[5][0].transpose(0, 1).contiguous(), topk,
+                                block_table=table[:1].clone())
+    assert torch.equal(paged, one)
+    del kc, vc, own, pools
+    torch.cuda.empty_cache()
 
 
 def test_decode_tree_defaults_are_a_full_chain():
