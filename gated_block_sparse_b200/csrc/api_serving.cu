@@ -128,6 +128,7 @@ sas_status sas_cache_append(const void* q, const int64_t* q_strides, void* qo, c
   REQUIRE(sum_dt == SAS_F32 || sum_dt == SAS_BF16, SAS_ERR_INVALID_ARG,
           "summary dtype must be SAS_F32 or SAS_BF16");
   REQUIRE(B <= 65535, SAS_ERR_UNSUPPORTED, "B must be <= 65535 (got %d)", B);
+  REQUIRE((q ? (long long)Hq : 0ll) + Hkv <= 65535, SAS_ERR_UNSUPPORTED, "at most 65535 heads");
   REQUIRE(q == nullptr || (inv_freq != nullptr && rows == nullptr), SAS_ERR_INVALID_ARG,
           "q needs inv_freq and no rows");
   if (slots)

@@ -14,10 +14,12 @@
 // fraction of the last turn, wrapping exactly, and the error is that of F,
 // 2^-53 f / 2 pi turns a position (2e-11 turns at 2^20 positions and f = 1).
 // The top 32 bits give the nearest quarter turn and an offset t of at most an
-// eighth (pi/4 radians), taken in two exact parts so that only its last
-// rounding remains. There the Taylor series of sin up to t^9 and of cos up to
-// t^10 are within 2e-9 and 2e-10: eleven multiply-adds, where a general
-// sincospi would reduce its argument again.
+// eighth (pi/4 radians), where the Taylor series of sin up to t^9 and of cos up
+// to t^10 are within 2e-9 and 2e-10. They are summed in fp64 (a dozen
+// operations at half the fp32 rate, half the instructions of two-part fp32
+// sums) and rounded once, amplitude included: a bf16 key that lands on the
+// other side of a rounding border moves its block's summary by far more than
+// fp32 resolves, and every bit here halves how often.
 #pragma once
 
 #include "common.cuh"
@@ -35,18 +37,16 @@ __device__ __forceinline__ void turn_sincos(unsigned long long F, int pos, float
   const uint32_t p = (uint32_t)(ph >> 32);
   const uint32_t quarter = (p + 0x20000000u) >> 30;  // nearest quarter turn (mod 4)
   const int off = (int)(p - (quarter << 30));        // [-2^29, 2^29): an eighth of a turn
-  // radians: off 2 pi / 2^32, the constant and off in two parts each
-  constexpr float R_HI = 1.4629180792671596e-09f;                                // 2 pi / 2^32
-  constexpr float R_LO = (float)(1.4629180792671596810513e-09 - (double)R_HI);
-  const float hi = (float)(off & ~63), lo = (float)(off & 63);
-  const float t = fmaf(hi, R_HI, fmaf(lo, R_HI, hi * R_LO)), q = t * t;
-  const float sn = fmaf(t * q, fmaf(q, fmaf(q, fmaf(q, 1.f / 362880, -1.f / 5040), 1.f / 120),
-                                    -1.f / 6), t);
-  const float cs = fmaf(q, fmaf(q, fmaf(q, fmaf(q, fmaf(q, -1.f / 3628800, 1.f / 40320),
-                                                -1.f / 720), 1.f / 24), -0.5f), 1.f);
-  const float a = (quarter & 1u) ? sn : cs, b = (quarter & 1u) ? cs : sn;
-  c = ((quarter == 1u || quarter == 2u) ? -a : a) * amp;
-  s = ((quarter & 2u) ? -b : b) * amp;
+  const double t = (double)off * 1.4629180792671596810513e-09;  // radians: 2 pi / 2^32
+  const double q = t * t;
+  const double sn =
+      fma(t * q, fma(q, fma(q, fma(q, 1.0 / 362880, -1.0 / 5040), 1.0 / 120), -1.0 / 6), t);
+  const double cs = fma(
+      q, fma(q, fma(q, fma(q, fma(q, -1.0 / 3628800, 1.0 / 40320), -1.0 / 720), 1.0 / 24), -0.5), 1.0);
+  const bool odd = quarter & 1u;
+  const double a = amp;
+  c = (float)((odd ? sn : cs) * ((quarter == 1u || quarter == 2u) ? -a : a));
+  s = (float)((odd ? cs : sn) * ((quarter & 2u) ? -a : a));
 }
 
 // A thread holds units of 2 VN elements of a head: VN pairs. VN = Vec16<T>::N
@@ -89,6 +89,12 @@ __device__ __forceinline__ void unit_offsets(int u, int rot, bool interleaved, i
   }
 }
 
+__device__ __forceinline__ void rotate_pair(float& x0, float& x1, float c, float s) {
+  const float y0 = x0 * c - x1 * s, y1 = x1 * c + x0 * s;
+  x0 = y0;
+  x1 = y1;
+}
+
 // Rotates the VN pairs of (a, b): element i of a with element i of b (half
 // layout), or neighbours within a, then within b (interleaved).
 template <int VN>
@@ -97,19 +103,12 @@ __device__ __forceinline__ void rotate_unit(float (&a)[VN], float (&b)[VN], cons
   if (VN > 1 && interleaved) {
 #pragma unroll
     for (int i = 0; i < VN / 2; ++i) {
-      const float a0 = a[2 * i], a1 = a[2 * i + 1], b0 = b[2 * i], b1 = b[2 * i + 1];
-      a[2 * i] = a0 * c[i] - a1 * s[i];
-      a[2 * i + 1] = a1 * c[i] + a0 * s[i];
-      b[2 * i] = b0 * c[VN / 2 + i] - b1 * s[VN / 2 + i];
-      b[2 * i + 1] = b1 * c[VN / 2 + i] + b0 * s[VN / 2 + i];
+      rotate_pair(a[2 * i], a[2 * i + 1], c[i], s[i]);
+      rotate_pair(b[2 * i], b[2 * i + 1], c[VN / 2 + i], s[VN / 2 + i]);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < VN; ++i) {
-      const float x0 = a[i], x1 = b[i];
-      a[i] = x0 * c[i] - x1 * s[i];
-      b[i] = x1 * c[i] + x0 * s[i];
-    }
+    for (int i = 0; i < VN; ++i) rotate_pair(a[i], b[i], c[i], s[i]);
   }
 }
 

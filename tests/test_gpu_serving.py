@@ -2,10 +2,10 @@
 
 Tolerances, derived before the first run. u = 2^-24 is fp32's half step,
 h = 2^-8 (bf16) or 2^-24 (fp32) the half step of a stored output.
-  rotation  sine and cosine are within 2^-23 (2 ulp of sincospif) plus 2^-24.3
-            (the rounded offset from a quarter turn) of exact, the amplitude
-            rounds once more (2^-24): below 2^-22.2 together; two products and
-            a sum add 2 u. |dy| <= A (|x0| + |x1|) 2^-21.5 + h |y|.
+  rotation  sine and cosine, amplitude included, are rounded once (u of their
+            value; the phase's last bit, 2^-32 turns, is 1.5e-9); one product and
+            the sum round once each. |dy| <= 3 u A (|x0| + |x1|) + 2^-29 A (...),
+            below A (|x0| + |x1|) 2^-22.3; + h |y|.
   tree      a logit of d products is within dz = (d + 8) u scale |q| max |k|
             (plus the same for the score inside a gate); weights move by
             2 dz, their sum and the output's accumulation over n keys by
@@ -53,7 +53,7 @@ def rot_tol(x, y, rot, interleaved, amp, dtype):
     for p in range(half):
         i, j = (2 * p, 2 * p + 1) if interleaved else (p, p + half)
         a[..., i] = a[..., j] = np.abs(x[..., i]) + np.abs(x[..., j])
-    t = amp * a * 2.0 ** -21.5
+    t = amp * a * 2.0 ** -22.3
     t[..., :rot] += HALF[dtype] * np.abs(y[..., :rot])
     return t
 
@@ -134,7 +134,7 @@ def test_rotary_reads_and_writes_strided_views(dtype, rot):
 def test_rotary_backward_is_the_gradient(inter):
     """L = sum(dy . R x): the inverse call on dy against differences of L along
     single inputs (L is linear in x, so a difference of any width is exact up
-    to rounding: 2 (2^-21.5 + u) A (|dy0| + |dy1|) per unit step)."""
+    to rounding: 2 (2^-22.3 + u) A (|dy0| + |dy1|) per unit step)."""
     B, H, N, d, rot = 1, 2, 5, 64, 48
     f, amp = rope.inv_freq(rot, scaling="parts", factor=4.0)
     f = f.to(DEV)
@@ -150,7 +150,7 @@ def test_rotary_backward_is_the_gradient(inter):
         y1 = sas.sas_rotary(x1, f, start=start, interleaved=inter, amplitude=amp)
         diff = float(((y1.double() - y0.double()) * dy.double()).sum())
         scale = amp * float(x[0, 1, 3].abs().max() + 1.0) * 2 * float(dy[0, 1, 3].abs().max())
-        assert abs(diff - float(dx[0, 1, 3, e])) <= 8 * scale * 2.0 ** -21.5
+        assert abs(diff - float(dx[0, 1, 3, e])) <= 8 * scale * 2.0 ** -22.3
 
 
 def test_rotary_tree_positions_and_bad_parents():
@@ -302,7 +302,7 @@ def test_cache_append_matches_the_oracle(c):
         big = np.abs(kc[..., :rot])
         pair = np.concatenate([big[..., rot // 2:], big[..., :rot // 2]], -1) if not inter else \
             big.reshape(*big.shape[:-1], -1, 2)[..., ::-1].reshape(big.shape)
-        tol = 2 * (big + pair) * 2.0 ** -21.5 + HALF[dtype] * big
+        tol = 2 * (big + pair) * 2.0 ** -22.3 + HALF[dtype] * big
         assert (np.abs(got - kc)[..., :rot] <= tol).all()
         assert np.array_equal(got[..., rot:], kc[..., rot:])
     # summaries: the mean of the keys as they are now stored, where a block was completed
