@@ -213,7 +213,7 @@ __device__ __forceinline__ float4 load_if(const float* p, bool on) {
 
 // Joins the splits: o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s. One CTA
 // per 8 / PARTS rows: a warp turns a row's maxima and sums into one factor per
-// split (lane s; at most 32 splits); thread (row, four columns, part) adds every
+// split (lane s); thread (row, four columns, part) adds every
 // PARTS-th split's partial output, four in flight, and the parts meet in shared
 // memory. A split that saw none of a row's keys has l = 0, and its partial
 // output is not read. Two rows or more side by side make every access a full
@@ -322,9 +322,14 @@ cudaError_t launch_tree_attn_simt(const TreeArgs& a, const TreeWs& w, int d, cud
 }
 
 // Splits of a kv group's units: as many as one wave of two CTAs an SM holds (a
-// second, shorter wave would cost another start), no more than the units that
-// the tokens can select, and at most one per lane of the join. Even two units
-// are split: a unit of one CTA costs as much as the join.
+// second, shorter wave costs another start: 8 x 128K 62 us a call, 69 with
+// twice the splits, 83 with one CTA an SM), and no more than the units that the
+// tokens can select. How many they do select is not known here, and splits
+// without a unit still cost the join: at most 20 (64K, 4 tokens, some 20 units:
+// 20.1 us a call, 22.2 with 32 splits, 22.0 with 8), or 24 of the fp32 kernel,
+// whose units take longer (20 tokens over 46 blocks: 51 us with 24 splits, 62
+// with 20). Even two units are split: a unit of one CTA costs as much as the
+// join.
 int tree_splits(int B, int Hq, int Hkv, int T, int N, int topk, int bf16) {
   const int tile = bf16 ? 128 : TA_ROWS;
   const long long tiles = ((long long)(Hq / Hkv) * T + tile - 1) / tile;
@@ -333,7 +338,8 @@ int tree_splits(int B, int Hq, int Hkv, int T, int N, int topk, int bf16) {
   if (units > N / SAS_BLOCK) units = N / SAS_BLOCK;
   long long ns = 2 * 148 / ctas;
   if (ns > units + 2) ns = units + 2;
-  if (ns > 32) ns = 32;
+  const int most = bf16 ? 20 : 24;
+  if (ns > most) ns = most;
   return ns < 1 ? 1 : (int)ns;
 }
 
