@@ -9,6 +9,7 @@
 // fp32 summaries take the six products h h, h m, m h, m m, h l, l h, bf16
 // summaries (one part) the three with qbar's parts; the MMAs accumulate in
 // fp32. What is dropped is below 2^-23 of a product, as an fp32 product rounds.
+// A score that comes out inf or NaN is computed again by fp32 FMAs.
 //
 // One CTA per (stretch of summaries, kv group, sequence), in tiles of 128
 // summaries: M = 128 blocks, K = d, and the three parts of qbar side by side
@@ -80,6 +81,34 @@ template <> struct Raw8<__nv_bfloat16> {
   __device__ __forceinline__ void parts(uint4 (&out)[1]) const { out[0] = a; }
 };
 
+// The score of one (summary, token) by fp32 FMAs, for one that the split products
+// made inf or NaN: a part of an infinity is NaN (inf - inf), as is its product
+// with a part that is 0, and a finite value past the largest bf16 rounds to an
+// infinite part. The mean query is the sum of its three parts in shared memory
+// (its first part alone where that is not finite).
+template <typename S, int D>
+__device__ __noinline__ float score_by_fma(const S* sum, const unsigned char* sb, int row, int NT) {
+  float dot = 0.f;
+#pragma unroll 2
+  for (int p = 0; p < D / 8; ++p) {
+    float q[8], m[8], l[8], x[8];
+    auto part = [&](int k, float (&y)[8]) {
+      Vec16<__nv_bfloat16>::load(
+          reinterpret_cast<const __nv_bfloat16*>(sb + sw_off(k * NT + row, p, 3 * NT)), y);
+    };
+    part(0, q);
+    part(1, m);
+    part(2, l);
+#pragma unroll
+    for (int i = 0; i < 8 / Vec16<S>::N; ++i)
+      load_cg(sum + p * 8 + i * Vec16<S>::N, x + i * Vec16<S>::N);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      dot = fmaf(fabsf(q[i]) < INFINITY ? q[i] + (m[i] + l[i]) : q[i], x[i], dot);
+  }
+  return dot;
+}
+
 // CTAs an SM: the 64 fp32 values that a thread loads ahead with STEP = 128 need
 // more than the 128 registers of two (a spilled one would be waited for).
 template <typename S, int STEP>
@@ -133,24 +162,22 @@ __global__ void __launch_bounds__(SC_THREADS, scores_ctas<S, STEP>()) k_tree_sco
   // Rows of a step, a step ahead; where they lie (row or page), a tile ahead. A row past the end reads the last one.
   Raw8<S> x[PER];
   int at[PER];
+  auto place_of = [&](int m) { return a.table ? __ldcg(a.table + (size_t)b * C + m) : m; };
+  auto sum_row = [&](int place) -> size_t {
+    if (!a.table) return group * C + place;
+    const bool ok = place >= 0 && place < a.npages;
+    if (!ok) atomicOr(err, kErrBadIndex);
+    return (size_t)(ok ? place : 0) * a.Hkv + r;
+  };
   auto place_tile = [&](int m0) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int m = min(m0 + tid / SP + i * (SC_THREADS / SP), m_hi - 1);
-      at[i] = a.table ? __ldcg(a.table + (size_t)b * C + m) : m;
-    }
+    for (int i = 0; i < PER; ++i)
+      at[i] = place_of(min(m0 + tid / SP + i * (SC_THREADS / SP), m_hi - 1));
   };
   auto load_step = [&](int step) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      size_t row = group * C + at[i];
-      if (a.table) {
-        const bool ok = at[i] >= 0 && at[i] < a.npages;
-        if (!ok) atomicOr(err, kErrBadIndex);
-        row = (size_t)(ok ? at[i] : 0) * a.Hkv + r;
-      }
-      x[i].load(static_cast<const S*>(a.ksum) + row * D + step * STEP + (tid % SP) * 8);
-    }
+    for (int i = 0; i < PER; ++i)
+      x[i].load(static_cast<const S*>(a.ksum) + sum_row(at[i]) * D + step * STEP + (tid % SP) * 8);
   };
   place_tile(m_lo);
   // B: qbar in three parts side by side, zeros behind the last token; its loads
@@ -259,13 +286,24 @@ __global__ void __launch_bounds__(SC_THREADS, scores_ctas<S, STEP>()) k_tree_sco
       tc::tmem_ld32(tm, y);
       tc::tmem_wait_ld();
       float* o = out + (size_t)t0 * CS + m;
+      uint32_t again = 0;  // tokens whose score is not finite
       if (m < m_hi) {
 #pragma unroll
         for (int t = 0; t < 32; ++t) {
           if (t0 + t >= nt) break;
-          *o = (v[t] + y[t]) * a.scale + 0.f;
+          const float s = (v[t] + y[t]) * a.scale + 0.f;
+          if (!(fabsf(s) < INFINITY)) again |= 1u << t;
+          *o = s;
           o += CS;
         }
+      }
+      if (again) {
+        const S* sum = static_cast<const S*>(a.ksum) + sum_row(place_of(m)) * D;
+        do {
+          const int t = __ffs(again) - 1;
+          again &= again - 1;
+          out[(size_t)(t0 + t) * CS + m] = score_by_fma<S, D>(sum, sb, t0 + t, NT) * a.scale + 0.f;
+        } while (again);
       }
     }
   }

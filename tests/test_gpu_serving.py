@@ -480,6 +480,41 @@ def test_decode_tree_ignores_what_a_token_does_not_see(dtype, paged):
         assert (got[b, :, m + 1:] == 3.0).all()
 
 
+@pytest.mark.parametrize("topk", [4, 40])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), 3.4e38])
+@pytest.mark.parametrize("dtype,sums,paged", [("bf16", "f32", False), ("bf16", "bf16", True),
+                                              ("f32", "f32", True), ("f32", "bf16", False)])
+def test_decode_tree_with_an_infinite_summary(dtype, sums, paged, bad, topk):
+    """A summary with one element that is infinite, or finite but past the
+    largest bf16 value, and queries of the other sign there: its score is -inf
+    (or hugely negative), its weight 0, and every result is finite, as in a
+    decode step. With queries of the same sign the gated rows of that head are
+    NaN for an infinity, and the other heads' are not."""
+    B, Hq, Hkv, d, T, N, e = 2, 4, 2, 128, 9, 1024, 5
+    if bad == 3.4e38 and sums == "bf16":
+        bad = 3.38e38  # the largest magnitude that stays finite in bf16
+    x = S.tree_case(41, B, Hq, Hkv, d, T, N, [900, 963], topk, dtype, sums, "tree", [9, 7])
+    # the other blocks have nothing there, so the planted levels keep their order
+    x["ksum"][..., e] = 0.0
+    x["ksum_t"][..., e] = 0.0
+    away = -np.sign(bad) * (np.abs(x["q"][..., e]) + 0.25)
+    t, v = S.rounded(away, dtype)
+    x["q_t"][..., e], x["q"][..., e] = t.reshape(away.shape), v.reshape(away.shape)
+    x["ksum_t"][0, 0, 3, e] = bad
+    x["ksum"][0, 0, 3, e] = float(x["ksum_t"][0, 0, 3, e])
+    out = torch.full((B, Hq, T, d), 3.0, dtype=S.TORCH[dtype], device=DEV)
+    idx = torch.full((B, Hkv, T, topk), -7, dtype=torch.int32, device=DEV)
+    tree_call(x, topk, 1, paged, out, idx)
+    check_tree(x, out, idx, topk, 1, dtype, sums)
+    if not np.isinf(bad):
+        return
+    x["q_t"][..., e], x["q"][..., e] = -x["q_t"][..., e], -x["q"][..., e]
+    out.fill_(3.0)
+    tree_call(x, topk, 1, paged, out, idx)
+    assert torch.isnan(out[0, :2, :9]).all()
+    assert torch.isfinite(out[0, 2:, :9]).all() and torch.isfinite(out[1, :, :7]).all()
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("N,topk", [(1024, 5), (700 * 64, 33), (1300 * 64, 128)])
 def test_decode_tree_ties_go_to_the_lower_block(dtype, N, topk):
