@@ -24,8 +24,10 @@
 // the sums). A value that is not finite in a block that only some rows keep
 // would reach the others the same way; such a row shows up as a sum that is
 // not finite, and repair_row computes it again key by key.
-// P is rounded to bf16 for its MMA (half a step is 2^-9 of a weight, and the
-// row's sum takes the unrounded weights); everything else is fp32.
+// P goes to its MMA in two bf16 parts, the upper half of its fp32 bits and the
+// rest rounded, which loses at most 2^-16 of a weight; one part loses 2^-8 and
+// left the results a sixth to a third further from their 64-bit values than
+// the rounding of the output alone. Everything else is fp32.
 // About 100 KB of shared memory and 256 TMEM columns, so two CTAs an SM. In the
 // loop a CTA takes 1.5 us a unit, 5.7 TB/s over all CTAs: HBM bounds 8 x 128K
 // (125 MB of kept blocks, 33 us with the start, the last CTAs of uneven groups
@@ -351,8 +353,8 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
         tc::fence_after_sync();
         const uint64_t vd = v_desc + (((j & 1) * 2 * L::TILE) >> 4);
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {  // P_j: columns 8 ks .. 8 ks + 7 of S_j's buffer
-          mma_tmem_a(tm_o, tm_s[j & 1] + 8 * ks, vd + ((ks * 2048) >> 4), ID_PV,
+        for (int ks = 0; ks < 8; ++ks) {  // P_j: its upper part, then its lower, 8 columns a step
+          mma_tmem_a(tm_o, tm_s[j & 1] + 8 * ks, vd + (((ks & 3) * 2048) >> 4), ID_PV,
                      (j > 0 || ks > 0) ? 1u : 0u);
         }
         tc::commit(&bars[B_OD]);
@@ -452,21 +454,24 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
       const float muse = grow ? mnew : m;
       const float off = bias - muse;
       float r0 = 0.f, r1 = 0.f;
-      uint32_t pk[NC / 2];
+      uint32_t pk[2][NC / 2];  // upper and lower parts of P, two keys a word
 #pragma unroll
       for (int i = 0; i < NC / 2; ++i) {
         float a0, a1;
         fma2c(a0, a1, z[2 * i], z[2 * i + 1], c1, off);
         const float p0 = tc::ex2(a0), p1 = tc::ex2(a1);
         add2(r0, r1, p0, p1);
-        __nv_bfloat162 h2 = __floats2bfloat162_rn(p0, p1);
-        pk[i] = *reinterpret_cast<uint32_t*>(&h2);
+        const uint32_t w0 = __float_as_uint(p0), w1 = __float_as_uint(p1);
+        pk[0][i] = __byte_perm(w0, w1, 0x7632);
+        const __nv_bfloat162 h2 = __floats2bfloat162_rn(p0 - __uint_as_float(w0 & 0xffff0000u),
+                                                        p1 - __uint_as_float(w1 & 0xffff0000u));
+        pk[1][i] = *reinterpret_cast<const uint32_t*>(&h2);
       }
       float rsum = r0 + r1;
       if (dead) {  // whatever the products were, NaN included
         rsum = 0.f;
 #pragma unroll
-        for (int i = 0; i < NC / 2; ++i) pk[i] = 0u;
+        for (int i = 0; i < NC / 2; ++i) pk[0][i] = pk[1][i] = 0u;
       }
       if (j > 0) {
         // PV_{j-1} done before O is rescaled. Waiting on every unit also keeps
@@ -491,13 +496,14 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
         l = rsum;
       }
       m = muse;
-      // P_j (64 bf16, two per column) over the first half of S_j's buffer
-      {
+      // P_j (two parts of 64 bf16, two per column) over S_j's buffer
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
         float pf[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i)  // zeros at the other copies' keys
-          pf[i] = copy == i / (NC / 2) ? __uint_as_float(pk[i % (NC / 2)]) : 0.f;
-        tc::tmem_st32(tm_s[st] + lane_off, pf);
+          pf[i] = copy == i / (NC / 2) ? __uint_as_float(pk[h][i % (NC / 2)]) : 0.f;
+        tc::tmem_st32(tm_s[st] + lane_off + 32 * h, pf);
       }
       tc::tmem_wait_st();
       tc::fence_before_sync();

@@ -480,6 +480,22 @@ def test_decode_tree_ignores_what_a_token_does_not_see(dtype, paged):
         assert (got[b, :, m + 1:] == 3.0).all()
 
 
+@pytest.mark.parametrize("Hq,d,T", [(8, 64, 40), (8, 128, 7), (4, 128, 13)])
+def test_decode_tree_keeps_the_weights_of_bf16_caches(Hq, d, T):
+    """A weight goes to its product in two bf16 parts: the upper half of its
+    bits, then the rest, below 2^-7 of it, rounded by half a step, so
+    w = 2^-16 in the bound above. Few keys and short queries keep the other
+    terms small: one part would pass the bound by several times."""
+    x = S.tree_case(500 + T, 3, Hq, 1, d, T, 128, [0, 3, 66], 1, "bf16", "f32", "tree")
+    x["q"] *= 0.125
+    x["q_t"] *= 0.125
+    got = np64(tree_call(x, 1, 1, False))
+    o, _, mass = SO.decode_tree(x["q"], x["kd"], x["vd"], x["kc"], x["vc"], x["lens"], x["ksum"],
+                                x["parents"], x["ntok"], 1)
+    tol = tree_tol(x, o, mass, 1, "bf16", "f32") + (2.0 ** -16 - 2.0 ** -8) * mass
+    assert (np.abs(got - o) <= tol).all()
+
+
 @pytest.mark.parametrize("topk", [4, 40])
 @pytest.mark.parametrize("bad", [float("inf"), float("-inf"), 3.4e38])
 @pytest.mark.parametrize("dtype,sums,paged", [("bf16", "f32", False), ("bf16", "bf16", True),
