@@ -105,8 +105,9 @@ __global__ void __launch_bounds__(TA_THREADS) k_tree_attn_simt(TreeArgs a, TreeW
       x.blk = u == u0 ? start_s : tree_next(bits, a.words, blk + 1);
     else
       x.nk = s.tail;
-    const size_t at =
-        x.nk > 0 ? tree_block_row(a, b, r, u < nu ? x.blk : s.c0, &g_tree_attn_err) * D : 0;
+    int place = x.nk > 0 ? tree_place(a, b, u < nu ? x.blk : s.c0, &g_tree_attn_err) : 0;
+    if (place < 0) place = x.nk = 0;  // its page is outside the pool
+    const size_t at = tree_block_row(a, b, r, place) * D;
     x.k = static_cast<const float*>(a.kc) + at;
     x.v = static_cast<const float*>(a.vc) + at;
     return x;
@@ -265,7 +266,8 @@ __global__ void __launch_bounds__(8 * D / 4) k_tree_join(TreeArgs a, TreeWs w) {
   __shared__ float4 part[PARTS > 1 ? PARTS - 1 : 1][ROWS * PER];
   const int b = blockIdx.z, r = blockIdx.y, lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int G = a.Hq / a.Hkv, row0 = blockIdx.x * ROWS;
-  const int nt = min(max(a.ntok ? __ldcg(a.ntok + b) : a.T, 0), a.T);
+  int n, nt;
+  tree_lengths(a, b, n, nt);
   grid_dep_wait();
   const int rows = G * nt;
   if (row0 >= rows) return;

@@ -145,7 +145,8 @@ struct RowState {
 // One row again, key by key, over the units of this split: only keys that the
 // row sees are read, so what other rows' blocks hold does not matter.
 template <int D>
-__device__ __noinline__ float2 repair_row(const TreeArgs& a, const TreeWs& w, const TreeSeq& s,
+__device__ __noinline__ float2 repair_row(const TreeArgs& a, const TreeWs& w, int nt, int tail,
+                                          int c0,
                                           const RowState& rs, const uint32_t* bits, int b, int r,
                                           const __nv_bfloat16* q, int nu, int u0, int u1,
                                           int start, float* out) {
@@ -166,14 +167,15 @@ __device__ __noinline__ float2 repair_row(const TreeArgs& a, const TreeWs& w, co
           bias = tree_bias(rs.info, __ldcg(w.scores + (group * a.T + rs.tok) * tree_stride(a.N / SAS_BLOCK) + blk),
                            blk, a.gated);
         } else {
-          nk = s.tail;
+          nk = tail;
         }
         if (nk == 0 || bias == -INFINITY) continue;
-        const size_t row = tree_block_row(a, b, r, u < nu ? blk : s.c0, nullptr);
+        const size_t row =
+            tree_block_row(a, b, r, max(tree_place(a, b, u < nu ? blk : c0, nullptr), 0));
         kp = kc + row * D;
         vp = vc + row * D;
       } else {
-        nk = s.nt;
+        nk = nt;
         kp = static_cast<const __nv_bfloat16*>(a.kd) + group * a.T * D;
         vp = static_cast<const __nv_bfloat16*>(a.vd) + group * a.T * D;
       }
@@ -276,6 +278,7 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
   const int nh = max(0, min(u1, nu) - u0), nunits = nsp + nh;
   const size_t R = (size_t)G * a.T, prow = (group * a.ns + split) * R + row0 + tid % RT;
   const int start = nh > 0 ? start_s : 0;
+  int tail = s.tail;  // its keys that are read: none where its page is outside the pool
   if (warp == 4) {
     // ---------------------------------------------------------------- producer
     if (lane < 2) {
@@ -290,7 +293,7 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
         blk = tree_next(bits, a.words, blk + 1);
         int y = 64 * blk, z = (int)group;
         if (a.table) {
-          z = tree_page(a, b, blk, err) * a.Hkv + r;
+          z = max(tree_place(a, b, blk, err), 0) * a.Hkv + r;  // a unit's page is in the pool
           y = 0;
         }
         unsigned char* dst = sm + L::KV + st * 2 * L::TILE + (kl ? 0u : L::TILE);
@@ -305,10 +308,13 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
     const int t = warp == 5 ? 128 + lane : tid;
     for (int j = 0; j < nsp; ++j) {
       const bool is_tail = has_tail && j == 0;
-      const int nk = is_tail ? s.tail : s.nt;
+      int nk = s.nt;
       const __nv_bfloat16 *kp, *vp;
       if (is_tail) {
-        const size_t at = tree_block_row(a, b, r, s.c0, err) * D;
+        const int place = tree_place(a, b, s.c0, err);
+        if (place < 0) tail = 0;
+        nk = tail;
+        const size_t at = tree_block_row(a, b, r, max(place, 0)) * D;
         kp = static_cast<const __nv_bfloat16*>(a.kc) + at;
         vp = static_cast<const __nv_bfloat16*>(a.vc) + at;
       } else {
@@ -318,7 +324,7 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
       unsigned char* st = sm + L::KV + j * 2 * L::TILE;
 #pragma unroll 2
       for (int e = t; e < 64 * PC; e += TT_THREADS - 32) {
-        const int row = e / PC, p = e % PC, from = min(row, nk - 1);
+        const int row = e / PC, p = e % PC, from = max(min(row, nk - 1), 0);
         cp_async16(st + sw_off(row, p, 64), kp + (size_t)from * D + p * 8, row < nk);
         cp_async16(st + L::TILE + sw_off(row, p, 64), vp + (size_t)from * D + p * 8, row < nk);
       }
@@ -408,7 +414,7 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
       const bool special = j < nsp;
       const bool is_tail = has_tail && j == 0;
       if (special) {
-        see = is_tail ? (1ull << s.tail) - 1ull : rs.anc;
+        see = is_tail ? (1ull << tail) - 1ull : rs.anc;
         if (rs.info.tail_bias == -INFINITY) see &= is_tail ? 0ull : ~rs.early;
       } else {
         bias = tree_bias(rs.info, score, blk, a.gated) * LOG2E;
@@ -587,7 +593,7 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
     if (valid && copy == 0) {
       float2 ml = make_float2(m, l);
       if (bad)
-        ml = repair_row<D>(a, w, s, rs, bits, b, r,
+        ml = repair_row<D>(a, w, s.nt, tail, s.c0, rs, bits, b, r,
                            q + (((size_t)b * a.Hq + r * G + row / s.nt) * a.T + rs.tok) * D, nu,
                            u0, u1, start, out);
       w.ml[prow] = ml;

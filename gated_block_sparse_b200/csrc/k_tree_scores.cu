@@ -68,6 +68,7 @@ template <> struct Raw8<float> {
     a = __ldcg(reinterpret_cast<const float4*>(p));
     b = __ldcg(reinterpret_cast<const float4*>(p) + 1);
   }
+  __device__ __forceinline__ void nan() { a.x = a.y = a.z = a.w = b.x = b.y = b.z = b.w = NAN; }
   __device__ __forceinline__ void parts(uint4 (&out)[3]) const {
     float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     split_bf16<3>(x, out);
@@ -78,6 +79,7 @@ template <> struct Raw8<__nv_bfloat16> {
   __device__ __forceinline__ void load(const __nv_bfloat16* p) {
     a = __ldcg(reinterpret_cast<const uint4*>(p));
   }
+  __device__ __forceinline__ void nan() { a.x = a.y = a.z = a.w = 0x7fff7fffu; }
   __device__ __forceinline__ void parts(uint4 (&out)[1]) const { out[0] = a; }
 };
 
@@ -140,8 +142,9 @@ __global__ void __launch_bounds__(SC_THREADS, scores_ctas<S, STEP>()) k_tree_sco
   grid_dep_wait();
   for (int i = m_lo / 32 + tid; i < min((m_lo + stretch) / 32, a.words); i += SC_THREADS)
     w.ubits[group * a.words + i] = 0u;
-  const int n = __ldcg(a.lens + b), ntk = a.ntok ? __ldcg(a.ntok + b) : a.T;
-  const int c0 = min(max(n, 0), a.N) / SAS_BLOCK, nt = min(max(ntk, 0), a.T);
+  int n, nt;
+  tree_lengths(a, b, n, nt);
+  const int c0 = n / SAS_BLOCK;
   const int m_hi = min(m_lo + stretch, c0);
   if (m_lo >= m_hi || nt == 0) return;
   if ((smem_u32(sm) & 1023u) != 0) {  // swizzled tiles need 1024-byte alignment
@@ -162,12 +165,10 @@ __global__ void __launch_bounds__(SC_THREADS, scores_ctas<S, STEP>()) k_tree_sco
   // Rows of a step, a step ahead; where they lie (row or page), a tile ahead. A row past the end reads the last one.
   Raw8<S> x[PER];
   int at[PER];
+  // A page outside the pool gives NaN scores, which the read-out turns to -inf.
   auto place_of = [&](int m) { return a.table ? __ldcg(a.table + (size_t)b * C + m) : m; };
   auto sum_row = [&](int place) -> size_t {
-    if (!a.table) return group * C + place;
-    const bool ok = place >= 0 && place < a.npages;
-    if (!ok) atomicOr(err, kErrBadIndex);
-    return (size_t)(ok ? place : 0) * a.Hkv + r;
+    return a.table ? (size_t)place * a.Hkv + r : group * C + place;
   };
   auto place_tile = [&](int m0) {
 #pragma unroll
@@ -176,8 +177,13 @@ __global__ void __launch_bounds__(SC_THREADS, scores_ctas<S, STEP>()) k_tree_sco
   };
   auto load_step = [&](int step) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-      x[i].load(static_cast<const S*>(a.ksum) + sum_row(at[i]) * D + step * STEP + (tid % SP) * 8);
+    for (int i = 0; i < PER; ++i) {
+      if (tree_page_ok(a, at[i]))
+        x[i].load(static_cast<const S*>(a.ksum) + sum_row(at[i]) * D + step * STEP +
+                  (tid % SP) * 8);
+      else
+        x[i].nan();
+    }
   };
   place_tile(m_lo);
   // B: qbar in three parts side by side, zeros behind the last token; its loads
@@ -298,11 +304,13 @@ __global__ void __launch_bounds__(SC_THREADS, scores_ctas<S, STEP>()) k_tree_sco
         }
       }
       if (again) {
-        const S* sum = static_cast<const S*>(a.ksum) + sum_row(place_of(m)) * D;
+        const int place = tree_place(a, b, m, err);
+        const S* sum = static_cast<const S*>(a.ksum) + (place < 0 ? 0 : sum_row(place) * D);
         do {
           const int t = __ffs(again) - 1;
           again &= again - 1;
-          out[(size_t)(t0 + t) * CS + m] = score_by_fma<S, D>(sum, sb, t0 + t, NT) * a.scale + 0.f;
+          out[(size_t)(t0 + t) * CS + m] =
+              place < 0 ? -INFINITY : score_by_fma<S, D>(sum, sb, t0 + t, NT) * a.scale + 0.f;
         } while (again);
       }
     }

@@ -120,7 +120,10 @@ __global__ void __launch_bounds__(THREADS) k_tree_select(TreeArgs a, TreeWs w) {
   const int Ci = s.c0 + (crossed ? 1 : 0);
   const int kk = min(a.topk, Ci);
   float virt = 0.f;
+  bool tail_in = true;  // the tail's page lies in the pool
   if (crossed) {
+    const int place = s.tail > 0 ? tree_place(a, b, s.c0, &g_tree_select_err) : 0;
+    tail_in = place >= 0;
     // Mean key of the tail's block as this path fills it: the tail's keys, then
     // the path's first ones. Thread (group, piece) sums every GRP-th key of one
     // 16-byte piece, all its loads in flight; the groups meet in shared memory.
@@ -132,7 +135,7 @@ __global__ void __launch_bounds__(THREADS) k_tree_select(TreeArgs a, TreeWs w) {
     }
     __syncthreads();
     const T* kc = static_cast<const T*>(a.kc) +
-                  (s.tail > 0 ? tree_block_row(a, b, r, s.c0, &g_tree_select_err) * D : 0);
+                  (s.tail > 0 && tail_in ? tree_block_row(a, b, r, place) * D : 0);
     const T* kd = static_cast<const T*>(a.kd) + group * a.T * D;
     float sum[VT];
 #pragma unroll
@@ -162,6 +165,7 @@ __global__ void __launch_bounds__(THREADS) k_tree_select(TreeArgs a, TreeWs w) {
       dot = qb * (1.0f / (float)G) * mean;
     }
     virt = block_sum<THREADS>(dot, red) * a.scale;
+    if (!tail_in) virt = -INFINITY;
   }
   if (tid == 0) {
     cnt_s = 0;
@@ -283,6 +287,11 @@ __global__ void __launch_bounds__(THREADS) k_tree_select(TreeArgs a, TreeWs w) {
   }
   const float lse = mx + logf(block_sum<THREADS>(sum, red));  // its barriers also close the list
   const int n = cnt_s;
+  // A kept block is one of the attention's units unless its page lies outside the
+  // pool; its score is then -inf (only such a one is looked up again).
+  auto is_unit = [&](int m, uint32_t key) {
+    return m < s.c0 && (key != score_key(-INFINITY) || tree_place(a, b, m, nullptr) >= 0);
+  };
   if (kk > 0 && n <= SEL_LIST) {
     // unique keys: a candidate's rank is the number of larger ones
     for (int e = tid; e < n; e += THREADS) {
@@ -291,7 +300,8 @@ __global__ void __launch_bounds__(THREADS) k_tree_select(TreeArgs a, TreeWs w) {
       if (rank < kk) {
         const int m = key_block(key);
         kept[rank] = m;
-        if (m < s.c0) atomicOr(&w.ubits[group * a.words + (m >> 5)], 1u << (m & 31));
+        if (is_unit(m, (uint32_t)(key >> 32)))
+          atomicOr(&w.ubits[group * a.words + (m >> 5)], 1u << (m & 31));
         if (rank == kk - 1) {
           th_s = (uint32_t)(key >> 32);
           last_s = m;
@@ -334,7 +344,7 @@ __global__ void __launch_bounds__(THREADS) k_tree_select(TreeArgs a, TreeWs w) {
     for (int m = lo; m < hi; ++m)
       if ((keys[m] > th || (keys[m] == th && m <= last)) && at < kk) {
         if (a.idx_out) a.idx_out[row * a.topk + at] = m;
-        if (m < s.c0) atomicOr(&w.ubits[group * a.words + (m >> 5)], 1u << (m & 31));
+        if (is_unit(m, keys[m])) atomicOr(&w.ubits[group * a.words + (m >> 5)], 1u << (m & 31));
         ++at;
       }
   }
@@ -346,7 +356,7 @@ __global__ void __launch_bounds__(THREADS) k_tree_select(TreeArgs a, TreeWs w) {
     t.th = th_s;
     t.last = last_s;
     t.tail_bias = 0.f;
-    if (crossed) t.tail_bias = kk > 0 ? tree_bias(t, virt, s.c0, a.gated) : -INFINITY;
+    if (crossed) t.tail_bias = kk > 0 && tail_in ? tree_bias(t, virt, s.c0, a.gated) : -INFINITY;
     w.rows[row] = t;
   }
 }

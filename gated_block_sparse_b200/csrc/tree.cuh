@@ -37,24 +37,32 @@ struct TreeSeq {
 
 __device__ __forceinline__ int tree_depth(unsigned long long anc) { return __popcll(anc) - 1; }
 
+// Cached and drafted tokens of sequence b: none drafted (the sequence is left
+// out) when a length lies outside the buffers.
+__device__ __forceinline__ bool tree_lengths(const TreeArgs& a, int b, int& n, int& nt) {
+  n = __ldcg(a.lens + b);
+  nt = a.ntok ? __ldcg(a.ntok + b) : a.T;
+  if (n >= 0 && n <= a.N && nt >= 0 && nt <= a.T) return true;
+  n = nt = 0;
+  return false;
+}
+
 // Lengths and ancestor masks of sequence b, by pointer jumping: after round e
 // a token's mask holds its 2^(e+1) nearest ancestors. The three loads go out
-// together. Lengths outside the buffers are clamped, a parent that is not
-// below its child is read as -1; both are reported when err is given. All
-// threads of the block (at least TREE_MAX) call it; it ends with a barrier.
-// No parents: a chain.
+// together. A sequence with a length outside the buffers has no tokens, a
+// parent that is not below its child is read as -1; both are reported when err
+// is given. All threads of the block (at least TREE_MAX) call it; it ends with
+// a barrier. No parents: a chain.
 __device__ __forceinline__ TreeSeq tree_load(const TreeArgs& a, int b, TreeShared& t,
                                              uint32_t* err) {
   const int i = threadIdx.x;
-  const int n = __ldcg(a.lens + b), nt = a.ntok ? __ldcg(a.ntok + b) : a.T;
+  TreeSeq s;
+  const bool fit = tree_lengths(a, b, s.n, s.nt);
   int p = i - 1;
   if (a.parents && i < a.T) p = __ldcg(a.parents + (size_t)b * a.T + i);
-  TreeSeq s;
-  s.n = min(max(n, 0), a.N);
-  s.nt = min(max(nt, 0), a.T);
   s.c0 = s.n / SAS_BLOCK;
   s.tail = s.n - s.c0 * SAS_BLOCK;
-  if (err && i == 0 && (s.n != n || s.nt != nt)) atomicOr(err, kErrBadIndex);
+  if (err && i == 0 && !fit) atomicOr(err, kErrBadIndex);
   unsigned long long m = 0;
   if (i < TREE_MAX) {
     if (i >= s.nt) p = -1;
@@ -90,20 +98,25 @@ __device__ __forceinline__ unsigned long long tree_early(const TreeShared& t) {
   return ((unsigned long long)t.early[1] << 32) | t.early[0];
 }
 
-// Page of logical block m of sequence b (an id outside the pool is reported
-// and replaced by page 0, as in the paged decode).
-__device__ __forceinline__ int tree_page(const TreeArgs& a, int b, int m, uint32_t* err) {
+// Where logical block m of sequence b lies: its page, or m itself in a
+// contiguous cache. -1 for an id outside the pool, which is reported: the block
+// is left out. The scores give it -inf and the selection keeps it out of the
+// units, so the attention meets it in the tail alone.
+__device__ __forceinline__ bool tree_page_ok(const TreeArgs& a, int page) {
+  return !a.table || (page >= 0 && page < a.npages);
+}
+__device__ __forceinline__ int tree_place(const TreeArgs& a, int b, int m, uint32_t* err) {
+  if (!a.table) return m;
   const int p = __ldcg(a.table + (size_t)b * (a.N / SAS_BLOCK) + m);
-  if (p >= 0 && p < a.npages) return p;
+  if (tree_page_ok(a, p)) return p;
   if (err) atomicOr(err, kErrBadIndex);
-  return 0;
+  return -1;
 }
 
-// First row of logical block m of head r, in rows of the cache.
-__device__ __forceinline__ size_t tree_block_row(const TreeArgs& a, int b, int r, int m,
-                                                 uint32_t* err) {
-  if (a.table) return ((size_t)tree_page(a, b, m, err) * a.Hkv + r) * SAS_BLOCK;
-  return ((size_t)b * a.Hkv + r) * a.N + (size_t)m * SAS_BLOCK;
+// First row of the block at `place` (>= 0) of head r, in rows of the cache.
+__device__ __forceinline__ size_t tree_block_row(const TreeArgs& a, int b, int r, int place) {
+  if (a.table) return ((size_t)place * a.Hkv + r) * SAS_BLOCK;
+  return ((size_t)b * a.Hkv + r) * a.N + (size_t)place * SAS_BLOCK;
 }
 
 // order-preserving map of a score to an unsigned integer (-0 becomes +0, so

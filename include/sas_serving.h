@@ -18,7 +18,8 @@
  * launch, calls may be captured in a CUDA graph). Numbers that live on the
  * device (lengths, parents, page ids, slots) cannot be checked on the host:
  * the kernels bound every one of them before they use it, report one that is
- * out of range through sas_device_status, and leave out what it named.
+ * out of range through sas_device_status, and leave out what it named, as each
+ * call says.
  */
 #ifndef SAS_SERVING_H
 #define SAS_SERVING_H
@@ -143,6 +144,13 @@ sas_status sas_cache_append(const void* q, const int64_t* q_strides, void* qo, c
  *   topk, gated, scale as sas_decode
  *   o [B][Hq][T][d] (dt); idx_out [B][Hkv][T][topk] int32 or NULL, logical
  *     blocks, ascending, -1 padded. Rows from ntok[b] on are left as they were.
+ * Reported and left out: a sequence with lens outside [0, N] or ntok outside
+ * [0, T] (all its rows stay as they were); a block whose page is outside
+ * [0, npages) (unlike in sas_decode_paged, no other page is read in its place:
+ * its score is -inf and none of its keys is attended to, also where it is the
+ * partly filled last one, and where a path fills that, the path's keys in it
+ * likewise; idx_out lists it where fewer than topk blocks score higher). A
+ * parent that is not below its child is reported and read as -1.
  * N a positive multiple of 64, at most 2^20; at most 8 query heads a kv head.
  * Workspace: sas_decode_tree_workspace_size() bytes.
  */

@@ -624,6 +624,99 @@ def test_decode_tree_reports_bad_parents_pages_and_lengths():
         assert sas.sas_device_status(clear=True)[0] == 5
 
 
+def masked_by_summary(x, dtype, sums, e=5):
+    """Column e of every query positive and of every summary 0, so that a summary
+    of -inf there gives a score of -inf in the oracle."""
+    x["ksum"][..., e] = 0.0
+    x["ksum_t"][..., e] = 0.0
+    t, v = S.rounded(np.abs(x["q"][..., e]) + 0.25, dtype)
+    x["q_t"][..., e] = t.reshape(x["q_t"][..., e].shape)
+    x["q"][..., e] = v.reshape(x["q"][..., e].shape)
+
+
+@pytest.mark.parametrize("where", [[10 ** 6, -4], [-1, 14]])
+@pytest.mark.parametrize("topk", [4, 40])
+@pytest.mark.parametrize("dtype,sums", [("bf16", "f32"), ("bf16", "bf16"), ("f32", "f32"),
+                                        ("f32", "bf16")])
+def test_decode_tree_leaves_out_pages_outside_the_pool(dtype, sums, topk, where):
+    """Blocks whose page ids lie outside the pool score -inf and are not attended
+    to; no other page (page 0 holds NaN) is read in their place."""
+    B, Hq, Hkv, d, T, N, e = 2, 4, 2, 64, 12, 512, 5
+    x = S.tree_case(61, B, Hq, Hkv, d, T, N, [420, 447], topk, dtype, sums, "tree", [12, 9])
+    masked_by_summary(x, dtype, sums)
+    kp, vp, ksp, table = S.to_pages(x, x["rng"], spare=0)
+    nan = lambda t: torch.cat([torch.full_like(t[:1], float("nan")), t]).to(DEV)[:17]
+    kp, vp, ksp, table = nan(kp), nan(vp), nan(ksp), table + 1
+    npages, gone = kp.shape[0], [(0, 1), (1, 2)]
+    for (b, m), w in zip(gone, where):
+        table[b, m] = w if w != 14 else npages
+        x["ksum"][b, :, m, e] = -np.inf
+    out = torch.full((B, Hq, T, d), 3.0, dtype=S.TORCH[dtype], device=DEV)
+    idx = torch.full((B, Hkv, T, topk), -7, dtype=torch.int32, device=DEV)
+    sas.sas_decode_tree(x["q_t"].to(DEV), x["kd_t"].to(DEV), x["vd_t"].to(DEV), kp, vp,
+                        i32(x["lens"]), ksp, topk, parents=i32(x["parents"]), ntok=i32(x["ntok"]),
+                        block_table=table.to(DEV), out=out, idx_out=idx)
+    st, msg = sas.sas_device_status(clear=True)
+    assert st == 5 and "k_tree_scores" in msg
+    check_tree(x, out, idx, topk, 1, dtype, sums)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_decode_tree_leaves_out_a_tail_page_outside_the_pool(dtype):
+    """Without a selection a token then attends to its path alone, as on an
+    empty cache; with one, a path that fills the tail's block does not keep it."""
+    B, Hq, Hkv, d, T, N, topk, e = 1, 4, 2, 64, 9, 256, 3, 5
+    x = S.tree_case(62, B, Hq, Hkv, d, T, N, [100], topk, dtype, "f32", "tree")
+    masked_by_summary(x, dtype, "f32")
+    kp, vp, ksp, table = S.to_pages(x, x["rng"], spare=0)
+    nan = lambda t: torch.cat([torch.full_like(t[:1], float("nan")), t]).to(DEV)
+    kp, vp, ksp, table = nan(kp), nan(vp), nan(ksp), table + 1
+    out = torch.full((B, Hq, T, d), 3.0, dtype=S.TORCH[dtype], device=DEV)
+
+    def call(lens, k, idx=None):
+        sas.sas_decode_tree(x["q_t"].to(DEV), x["kd_t"].to(DEV), x["vd_t"].to(DEV), kp, vp,
+                            i32(lens), ksp, k, parents=i32(x["parents"]),
+                            block_table=table.to(DEV), out=out, idx_out=idx)
+        assert sas.sas_device_status(clear=True)[0] == 5
+    table[0, 1] = -9
+    call([100], 0)
+    check_tree(dict(x, lens=np.array([0])), out, torch.empty((B, Hkv, T, 0), dtype=torch.int32), 0, 1,
+               dtype, "f32")
+    # 127 cached tokens: every token but the roots has filled block 1, which
+    # stands at -inf in the oracle through the summary that the path gives it
+    deep = SO.depths(x["parents"])[0] > 0
+    assert deep.any()
+    x["lens"] = np.array([127])
+    idx = torch.full((B, Hkv, T, topk), -7, dtype=torch.int32, device=DEV)
+    call([127], topk, idx)
+
+    def gone(mean):
+        mean = mean.copy()
+        mean[..., e] = -np.inf
+        return mean
+    o, want, mass = SO.decode_tree(x["q"], x["kd"], x["vd"], x["kc"], x["vc"], x["lens"], x["ksum"],
+                                   x["parents"], x["ntok"], topk, 1, gone)
+    tol = tree_tol(x, o, mass, topk, dtype, "f32")
+    assert (np.abs(np64(out) - o) <= tol)[:, :, deep].all()
+    assert np.array_equal(idx.cpu().numpy()[:, :, deep], want[:, :, deep])
+
+
+@pytest.mark.parametrize("topk", [0, 3])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens,ntok", [(513, 8), (-1, 8), (400, 9), (400, -2)])
+def test_decode_tree_leaves_out_impossible_lengths(lens, ntok, dtype, topk):
+    B, Hq, Hkv, d, T, N = 2, 4, 1, 64, 8, 512
+    x = S.tree_case(63, B, Hq, Hkv, d, T, N, [400, 300], max(topk, 1), dtype, "f32", "chain")
+    x["lens"], x["ntok"] = np.array([lens, 300]), np.array([ntok, 7])
+    out = torch.full((B, Hq, T, d), 3.0, dtype=S.TORCH[dtype], device=DEV)
+    idx = torch.full((B, Hkv, T, topk), -7, dtype=torch.int32, device=DEV)
+    tree_call(x, topk, 1, False, out, idx)
+    assert sas.sas_device_status(clear=True)[0] == 5
+    assert (out[0] == 3.0).all() and (idx[0] == -7).all()
+    y = {n: (v[1:] if n != "rng" else v) for n, v in x.items()}
+    check_tree(y, out[1:], idx[1:], topk, 1, dtype, "f32")
+
+
 def test_binding_refuses_other_types_shapes_and_layouts():
     q = torch.zeros(1, 2, 4, 64, device=DEV)
     f = torch.ones(16, device=DEV)
