@@ -23,7 +23,7 @@
 // behind the last key (whatever the cache holds there, 0 * NaN would reach
 // the sums). A value that is not finite in a block that only some rows keep
 // would reach the others the same way; such a row shows up as a sum that is
-// not finite, and repair_row computes it again key by key.
+// not finite, and its warp computes it again (repair_row).
 // P goes to its MMA in two bf16 parts, the upper half of its fp32 bits and the
 // rest rounded, which loses at most 2^-16 of a weight; one part loses 2^-8 and
 // left the results a sixth to a third further from their 64-bit values than
@@ -136,73 +136,115 @@ __device__ __forceinline__ void tmem_row(uint32_t taddr, float (&z)[N]) {
   tc::tmem_wait_ld();
 }
 
+// What the repair of a row needs: the row and the split that it is computed for.
 struct RowState {
   unsigned long long anc, early;
   TreeRow info;
   int tok;
 };
+struct SplitState {
+  const uint32_t* bits;
+  int b, r, nt, tail, c0, nu, u0, u1, start;
+};
 
-// One row again, key by key, over the units of this split: only keys that the
-// row sees are read, so what other rows' blocks hold does not matter.
+// One row again, over the units of this split, by a whole warp: only keys that
+// the row sees are read, so what other rows' blocks hold does not matter. A lane
+// takes two keys of a unit for q . k and D / 32 columns for p v. A visible key
+// whose logit is NaN or +inf makes the row NaN, and the units behind it are not
+// read; the tail and the drafted tokens, which many rows see, come first. About
+// 5 us a row and unit: a NaN in a value of the tail, seen by every row, makes a
+// call of 64K and 4 tokens 61 us (27 without, launched one by one), one of 512K
+// and 64 tokens 1.6 ms (68); a NaN in its key 37 and 320 us. One thread a row
+// took 0.9 and 21 ms.
 template <int D>
-__device__ __noinline__ float2 repair_row(const TreeArgs& a, const TreeWs& w, int nt, int tail,
-                                          int c0,
-                                          const RowState& rs, const uint32_t* bits, int b, int r,
-                                          const __nv_bfloat16* q, int nu, int u0, int u1,
-                                          int start, float* out) {
+__device__ __noinline__ float2 repair_row(const TreeArgs& a, const TreeWs& w, const SplitState& s,
+                                          const RowState& rs, const __nv_bfloat16* q, float* out) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  const size_t group = (size_t)s.b * a.Hkv + s.r, R = (size_t)(a.Hq / a.Hkv) * a.T;
   const __nv_bfloat16* kc = static_cast<const __nv_bfloat16*>(a.kc);
   const __nv_bfloat16* vc = static_cast<const __nv_bfloat16*>(a.vc);
-  const size_t group = (size_t)b * a.Hkv + r, R = (size_t)(a.Hq / a.Hkv) * a.T;
-  float m = -1e30f, l = 0.f;
-  for (int c = 0; c < D; ++c) out[tree_part_at(c, R)] = 0.f;
-  for (int pass = 0; pass < 2; ++pass) {  // the maximum first, then the sums
-    int blk = -1;
-    for (int u = u0; u < u1; ++u) {
-      const __nv_bfloat16 *kp, *vp;
-      int nk = SAS_BLOCK;
-      float bias = rs.info.tail_bias;
-      if (u <= nu) {
-        if (u < nu) {
-          blk = u == u0 ? start : tree_next(bits, a.words, blk + 1);
-          bias = tree_bias(rs.info, __ldcg(w.scores + (group * a.T + rs.tok) * tree_stride(a.N / SAS_BLOCK) + blk),
-                           blk, a.gated);
-        } else {
-          nk = tail;
-        }
-        if (nk == 0 || bias == -INFINITY) continue;
-        const size_t row =
-            tree_block_row(a, b, r, max(tree_place(a, b, u < nu ? blk : c0, nullptr), 0));
-        kp = kc + row * D;
-        vp = vc + row * D;
+  const float* sc = w.scores + (group * a.T + rs.tok) * tree_stride(a.N / SAS_BLOCK);
+  float m = -1e30f, l = 0.f, acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  int blk = s.start - 1;
+  const int special = s.u1 - max(s.u0, min(s.nu, s.u1));
+  for (int i = 0; i < s.u1 - s.u0; ++i) {
+    const int u = i < special ? s.u1 - special + i : s.u0 + i - special;
+    const bool drafted = u > s.nu;
+    size_t at = group * a.T;  // first row of the unit
+    unsigned long long see = rs.anc, gate = rs.early;  // keys seen, those with the gate's bias
+    float bias = rs.info.tail_bias;
+    if (!drafted) {
+      see = gate = ~0ull;
+      if (u < s.nu) {
+        blk = tree_next(s.bits, a.words, blk + 1);
+        bias = tree_bias(rs.info, __ldcg(sc + blk), blk, a.gated);
       } else {
-        nk = nt;
-        kp = static_cast<const __nv_bfloat16*>(a.kd) + group * a.T * D;
-        vp = static_cast<const __nv_bfloat16*>(a.vd) + group * a.T * D;
+        see = (1ull << s.tail) - 1ull;
       }
-      for (int j = 0; j < nk; ++j) {
-        float bj = bias;
-        if (u > nu) {
-          if (!(rs.anc >> j & 1ull)) continue;
-          if (!(rs.early >> j & 1ull)) bj = 0.f;
-          if (bj == -INFINITY) continue;
-        }
+    }
+    if (bias == -INFINITY) see &= ~gate;
+    if (see == 0ull) continue;
+    if (!drafted)
+      at = tree_block_row(a, s.b, s.r,
+                          max(tree_place(a, s.b, u < s.nu ? blk : s.c0, nullptr), 0));
+    const __nv_bfloat16* kp = (drafted ? static_cast<const __nv_bfloat16*>(a.kd) : kc) + at * D;
+    const __nv_bfloat16* vp = (drafted ? static_cast<const __nv_bfloat16*>(a.vd) : vc) + at * D;
+    float p[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int j = lane + 32 * h;
+      p[h] = -INFINITY;
+      if (see >> j & 1ull) {
         float z = 0.f;
-        for (int c = 0; c < D; ++c) z = fmaf(to_f(__ldcg(q + c)), to_f(__ldcg(kp + (size_t)j * D + c)), z);
-        z = (z * a.scale + bj) * LOG2E;
-        if (pass == 0) {
-          m = fmaxf(m, z);
-        } else {
-          const float p = exp2f(z - m);
-          l += p;
-          if (p != 0.f)
-            for (int c = 0; c < D; ++c) {
-              float& x = out[tree_part_at(c, R)];
-              x = fmaf(p, to_f(__ldcg(vp + (size_t)j * D + c)), x);
-            }
+#pragma unroll 8
+        for (int c = 0; c < D; c += 8) {
+          float x[8], y[8];
+          load_cg(q + c, x);
+          load_cg(kp + (size_t)j * D + c, y);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) z = fmaf(x[k], y[k], z);
+        }
+        p[h] = (z * a.scale + (gate >> j & 1ull ? bias : 0.f)) * LOG2E;
+      }
+    }
+    if (__any_sync(0xffffffffu, !(p[0] < INFINITY && p[1] < INFINITY))) {
+      l = NAN;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = NAN;
+      break;
+    }
+    const float mx = warp_max(fmaxf(p[0], p[1]));
+    if (mx == -INFINITY) continue;
+    const float mn = fmaxf(m, mx), alpha = exp2f(m - mn);
+    m = mn;
+    p[0] = exp2f(p[0] - mn);
+    p[1] = exp2f(p[1] - mn);
+    l = l * alpha + warp_sum(p[0] + p[1]);
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = alpha == 0.f ? 0.f : acc[e] * alpha;  // not 0 * inf
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll 16
+      for (int j = 0; j < 32; ++j) {
+        const float pj = __shfl_sync(0xffffffffu, p[h], j);
+        if (pj == 0.f) continue;  // not seen: not read
+        const uint32_t* v =
+            reinterpret_cast<const uint32_t*>(vp + (size_t)(32 * h + j) * D + lane * E);
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          const uint32_t x = __ldcg(v + e / 2);
+          acc[e] = fmaf(pj, __uint_as_float(x << 16), acc[e]);
+          acc[e + 1] = fmaf(pj, __uint_as_float(x & 0xffff0000u), acc[e + 1]);
         }
       }
     }
   }
+  out += tree_part_at(lane * E, R);
+#pragma unroll
+  for (int e = 0; e < E; ++e) out[e] = acc[e];
   return make_float2(m, l);
 }
 
@@ -590,13 +632,25 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
         }
       }
     }
-    if (valid && copy == 0) {
-      float2 ml = make_float2(m, l);
-      if (bad)
-        ml = repair_row<D>(a, w, s.nt, tail, s.c0, rs, bits, b, r,
-                           q + (((size_t)b * a.Hq + r * G + row / s.nt) * a.T + rs.tok) * D, nu,
-                           u0, u1, start, out);
-      w.ml[prow] = ml;
+    if (valid && !bad && copy == 0) w.ml[prow] = make_float2(m, l);
+    // Every copy's warp knows the bad rows; each takes every COPIES-th of them.
+    const uint32_t again = __ballot_sync(0xffffffffu, valid && bad && lane % COPIES == copy);
+    if (again) {
+      __syncwarp();  // what a row's own thread wrote to `out` is overwritten
+      const SplitState ss{bits, b, r, s.nt, tail, s.c0, nu, u0, u1, start};
+      const size_t at = (group * a.ns + split) * R;
+      for (uint32_t todo = again; todo; todo &= todo - 1) {
+        const int row1 = row0 + (warp * 32 + __ffs(todo) - 1) % RT;
+        RowState r1;
+        r1.tok = row1 % s.nt;
+        r1.anc = tree.anc[r1.tok];
+        r1.early = rs.early;
+        r1.info = tree_row(a, w, s, group, r1.tok, r1.anc);
+        const float2 ml = repair_row<D>(
+            a, w, ss, r1, q + (((size_t)b * a.Hq + r * G + row1 / s.nt) * a.T + r1.tok) * D,
+            w.part + at * D + (size_t)row1 * 4);
+        if (lane == 0) w.ml[at + row1] = ml;
+      }
     }
   }
   tc::fence_before_sync();

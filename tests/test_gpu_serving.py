@@ -717,6 +717,48 @@ def test_decode_tree_leaves_out_impossible_lengths(lens, ntok, dtype, topk):
     check_tree(y, out[1:], idx[1:], topk, 1, dtype, "f32")
 
 
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hq,T", [(4, 5), (8, 7), (8, 17)])  # 20, 56 and 136 rows a group
+def test_decode_tree_of_caches_with_bad_values(Hq, T, d, paged):
+    """Infinities and NaN where tokens do see them: a value of a kept block and
+    one of the tail reach their column alone, a NaN key makes the rows that keep
+    its block NaN and no others, also across splits and copies of the rows."""
+    B, Hkv, N, topk = 2, 1, 1024, 4
+    x = S.tree_case(71, B, Hq, Hkv, d, T, N, [900, 963], topk, "bf16", "f32", "tree", [T, T - 1])
+    _, sel, _ = SO.decode_tree(x["q"], x["kd"], x["vd"], x["kc"], x["vc"], x["lens"], x["ksum"],
+                               x["parents"], x["ntok"], topk)
+    inf, nan = float("inf"), float("nan")
+    for b in range(B):
+        n = int(x["lens"][b])
+        blocks = [set(sel[b, 0, i][sel[b, 0, i] >= 0].tolist()) for i in range(int(x["ntok"][b]))]
+        some = sorted(s for s in set.union(*blocks) - set.intersection(*blocks) if s < n // 64)
+        both = sorted(s for s in set.intersection(*blocks) if s < n // 64)
+        assert some
+        for name, at, c, v in [("kc", 64 * some[0] + 9, 3, nan), ("vc", 64 * some[-1] + 33, 11, inf),
+                               ("vc", n - 2, 7, -inf), ("vd", T - 2, 20, inf)] + \
+                [("vc", 64 * m + 63, 30, inf) for m in both[:1]]:
+            x[name][b, 0, at, c] = v
+            x[name + "_t"][b, 0, at, c] = v
+    out = torch.full((B, Hq, T, d), 3.0, dtype=torch.bfloat16, device=DEV)
+    tree_call(x, topk, 1, paged, out)
+    with np.errstate(invalid="ignore"):
+        o, _, mass = SO.decode_tree(x["q"], x["kd"], x["vd"], x["kc"], x["vc"], x["lens"],
+                                    x["ksum"], x["parents"], x["ntok"], topk)
+    got = np64(out)
+    finite = dict(x, kc=np.nan_to_num(x["kc"]))
+    tol = tree_tol(finite, np.nan_to_num(o, posinf=0, neginf=0),
+                   np.nan_to_num(mass, posinf=0, neginf=0), topk, "bf16", "f32")
+    for b in range(B):
+        m = int(x["ntok"][b])
+        g, r = got[b, :, :m], o[b, :, :m]
+        fin = np.isfinite(r)
+        assert fin.any() and np.isnan(r).any() and np.isinf(r).any()
+        assert np.array_equal(np.isnan(g), np.isnan(r))
+        assert np.array_equal(g[np.isinf(r)], r[np.isinf(r)])
+        assert (np.abs(g[fin] - r[fin]) <= tol[b, :, :m][fin]).all()
+
+
 def test_binding_refuses_other_types_shapes_and_layouts():
     q = torch.zeros(1, 2, 4, 64, device=DEV)
     f = torch.ones(16, device=DEV)
