@@ -11,10 +11,12 @@
 // theta reaches 5e5 radians at the end of a 512K context, where an fp32
 // product is off by up to 0.03 radians. So the frequency is kept in turns as a
 // 64-bit binary fraction, F = frac(f / 2 pi) 2^64: pos * F modulo 2^64 is the
-// fraction of the last turn, wrapping exactly, and the error is that of F,
-// 2^-53 f / 2 pi turns a position (2e-11 turns at 2^20 positions and f = 1).
-// The top 32 bits give the nearest quarter turn and an offset t of at most an
-// eighth (pi/4 radians), where the Taylor series of sin up to t^9 and of cos up
+// fraction of the last turn, wrapping exactly, and the error is that of F, two
+// fp64 roundings and the fraction's last bit: 2^-52 f / 2 pi + 2^-64 turns a
+// position (4e-11 turns at 2^20 positions and f = 1). The top bits give the nearest quarter turn, and all 64 an offset t
+// of at most an eighth (pi/4 radians, kept to fp64's 53 bits, so that a sine or
+// cosine near 0 is as exact as any other; 32 bits of it would be 1.5e-9 off), where
+// the Taylor series of sin up to t^9 and of cos up
 // to t^10 are within 2e-9 and 2e-10. They are summed in fp64 (a dozen
 // operations at half the fp32 rate, half the instructions of two-part fp32
 // sums) and rounded once, amplitude included: a bf16 key that lands on the
@@ -34,10 +36,10 @@ __device__ __forceinline__ unsigned long long turns_u64(float f) {
 __device__ __forceinline__ void turn_sincos(unsigned long long F, int pos, float amp, float& c,
                                             float& s) {
   const unsigned long long ph = F * (unsigned long long)(long long)pos;
-  const uint32_t p = (uint32_t)(ph >> 32);
-  const uint32_t quarter = (p + 0x20000000u) >> 30;  // nearest quarter turn (mod 4)
-  const int off = (int)(p - (quarter << 30));        // [-2^29, 2^29): an eighth of a turn
-  const double t = (double)off * 1.4629180792671596810513e-09;  // radians: 2 pi / 2^32
+  const uint32_t quarter = ((uint32_t)(ph >> 32) + 0x20000000u) >> 30;  // nearest one (mod 4)
+  // [-2^61, 2^61): an eighth of a turn, as the difference wraps
+  const long long off = (long long)(ph - ((unsigned long long)quarter << 62));
+  const double t = (double)off * (1.4629180792671596810513e-09 / 4294967296.0);  // 2 pi / 2^64
   const double q = t * t;
   const double sn =
       fma(t * q, fma(q, fma(q, fma(q, 1.0 / 362880, -1.0 / 5040), 1.0 / 120), -1.0 / 6), t);

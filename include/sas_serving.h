@@ -39,8 +39,9 @@ extern "C" {
  * with (x0, x1) = elements (p, p + rot/2) of the head, or (2p, 2p + 1) when
  * interleaved = 1, and A = amplitude. Elements from rot on are passed through.
  * inverse = 1 turns by -theta: with the same A it is the transpose, so it
- * takes dy to dx. theta is exact to 2e-11 turns at 2^20 positions whatever
- * the position (no fp32 product); a long context is set by inv_freq and A.
+ * takes dy to dx. theta is exact to 4e-17 inv_freq + 6e-20 turns a position (no
+ * fp32 product; 4e-11 turns at 2^20 positions and 1 radian a position); a long
+ * context is set by inv_freq and A.
  *   q [B][Hq][N][d] (dt), k [B][Hkv][N][d] or NULL (with Hkv = 0), read
  *     through element strides {batch, head, token}; qo, ko likewise. A stride
  *     pointer (host memory, three values) of NULL means contiguous. Rows of d

@@ -170,6 +170,30 @@ def test_rotary_tree_positions_and_bad_parents():
     assert torch.equal(got, sas.sas_rotary(q, f, pos=i32(start[:, None] + SO.depths(par))))
 
 
+@pytest.mark.parametrize("rot", [64, 20])  # vectors and single elements
+def test_rotary_near_quarter_turns(rot):
+    """Angles at odd quarter turns, where the cosine is as small as the rounding of
+    the fp32 frequency leaves it (1e-8 to 1e-3): x = (1, 0) turns to (cos, sin).
+    Bound: 2^-52 of the angle, and one rounding of the cosine and of its product
+    with 1 (2 u of it). The frequency in turns is a 64-bit fraction whose last bit
+    is cut, so p positions add up to p 2^-64 turns, 2 pi p 2^-64 radians: a term
+    of its own, since a small frequency's 2^-52 is less than that bit."""
+    d, pos = 64, np.array([1, 3, 5, 4097, 65535, 1048575], dtype=np.int64)
+    f = np.full(rot // 2, 0.3, dtype=np.float32)
+    for i, p in enumerate(pos):
+        f[i] = np.float32(np.pi / 2 / p)
+    x = np.zeros((1, 1, len(pos), d))
+    x[..., :rot // 2] = 1.0
+    y = np64(sas.sas_rotary(torch.from_numpy(x).float().to(DEV), torch.from_numpy(f).to(DEV),
+                            pos=i32(pos[None])))[0, 0]
+    for i, p in enumerate(pos):
+        theta = np.longdouble(f[i]) * np.longdouble(p)
+        want = float(np.cos(theta))
+        assert 0 < abs(want) < 1e-3
+        tol = 2 * U * abs(want) + float(theta) * 2.0 ** -52 + 2 * np.pi * p * 2.0 ** -64
+        assert abs(y[i, i] - want) <= tol, (p, y[i, i], want)
+
+
 # ---------------------------------------------------------------- page tables
 def page_case(seed, B, T, top, width=None, short=0):
     rng = np.random.Generator(np.random.PCG64(seed))
