@@ -96,12 +96,11 @@ __global__ void __launch_bounds__(AP_THREADS, 2) k_append(AppendArgs a) {
   int e0, e1;
   unit_offsets<VN>(u, a.rot, a.interleaved, e0, e1);
   if (turned) {
-    unsigned long long F[VN];
-    unit_turns<VN>(a.inv_freq, u, F);
+    const UnitTurns<VN> turns(a.inv_freq, u);
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
       const int j = jb + g + i * RG;
-      if (j >= 0 && j < a.T) unit_sincos<VN>(F, len + j, a.amp, c[i], s[i]);
+      if (j >= 0 && j < a.T) turns.sincos(len + j, a.amp, c[i], s[i]);
     }
   }
   const int Hk = a.Hkv, Hall = Hk + (a.q ? a.Hq : 0);

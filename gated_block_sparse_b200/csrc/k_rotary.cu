@@ -57,9 +57,7 @@ __global__ void __launch_bounds__(RT_THREADS) k_rotary(
   const bool turned = u < rot / (2 * VN);
   float c[VN], s[VN];
   if (turned) {
-    unsigned long long F[VN];
-    unit_turns<VN>(inv_freq, u, F);
-    unit_sincos<VN>(F, p, amp, c, s);
+    UnitTurns<VN>(inv_freq, u).sincos(p, amp, c, s);
     if (inverse) {
 #pragma unroll
       for (int i = 0; i < VN; ++i) s[i] = -s[i];

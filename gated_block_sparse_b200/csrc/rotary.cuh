@@ -24,6 +24,8 @@
 // fp32 resolves, and every bit here halves how often.
 #pragma once
 
+#include <math.h>
+
 #include "common.cuh"
 
 namespace sas {
@@ -115,18 +117,26 @@ __device__ __forceinline__ void rotate_unit(float (&a)[VN], float (&b)[VN], cons
 }
 
 // Turns per position of the VN pairs of rotated unit u: pairs u VN .. u VN +
-// VN - 1 in both layouts.
+// VN - 1 in both layouts. A frequency that is not finite has no turns: its bit
+// of `bad` is set, and the pair's sine and cosine are NaN.
 template <int VN>
-__device__ __forceinline__ void unit_turns(const float* __restrict__ inv_freq, int u,
-                                           unsigned long long (&F)[VN]) {
+struct UnitTurns {
+  unsigned long long F[VN];
+  uint32_t bad;
+
+  __device__ __forceinline__ UnitTurns(const float* __restrict__ inv_freq, int u) : bad(0) {
 #pragma unroll
-  for (int i = 0; i < VN; ++i) F[i] = turns_u64(__ldg(inv_freq + u * VN + i));
-}
-template <int VN>
-__device__ __forceinline__ void unit_sincos(const unsigned long long (&F)[VN], int pos, float amp,
-                                            float (&c)[VN], float (&s)[VN]) {
+    for (int i = 0; i < VN; ++i) {
+      const float f = __ldg(inv_freq + u * VN + i);
+      if (!(fabsf(f) < INFINITY)) bad |= 1u << i;
+      F[i] = turns_u64(f);
+    }
+  }
+  __device__ __forceinline__ void sincos(int pos, float amp, float (&c)[VN],
+                                         float (&s)[VN]) const {
 #pragma unroll
-  for (int i = 0; i < VN; ++i) turn_sincos(F[i], pos, amp, c[i], s[i]);
-}
+    for (int i = 0; i < VN; ++i) turn_sincos(F[i], pos, bad >> i & 1u ? NAN : amp, c[i], s[i]);
+  }
+};
 
 }  // namespace sas

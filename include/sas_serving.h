@@ -47,7 +47,8 @@ extern "C" {
  *     pointer (host memory, three values) of NULL means contiguous. Rows of d
  *     elements are contiguous. Input strides may be 0 (shared rows), output
  *     rows must not overlap; qo = q with equal strides rotates in place.
- *   inv_freq [rot/2] fp32, radians per position; rot even, 2 <= rot <= d
+ *   inv_freq [rot/2] fp32, radians per position (an entry that is not finite
+ *     turns its pair to NaN); rot even, 2 <= rot <= d
  *   pos [B][N] int32: the positions; or NULL, then position = start[b]
  *     (start [B] int32, NULL = 0) + n, or + the depth of token n when
  *     parents [B][N] int32 is given (the tree of sas_decode_tree: a parent is

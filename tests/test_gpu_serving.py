@@ -194,6 +194,28 @@ def test_rotary_near_quarter_turns(rot):
         assert abs(y[i, i] - want) <= tol, (p, y[i, i], want)
 
 
+@pytest.mark.parametrize("dtype,rot", [("bf16", 64), ("f32", 64), ("bf16", 12)])
+def test_rotary_of_frequencies_that_are_not_finite(dtype, rot):
+    """An infinite or NaN frequency has no angle: its pair is NaN, in the rotation
+    and in the cache write, and the other pairs are as before."""
+    d, N = 64, 70
+    g = torch.Generator().manual_seed(rot)
+    x = torch.randn((1, 2, N, d), generator=g).to(S.TORCH[dtype]).to(DEV)
+    f = rope.inv_freq(rot)[0]
+    want = sas.sas_rotary(x, f.to(DEV))
+    gone = torch.zeros(d, dtype=torch.bool)
+    for p, v in ((0, float("nan")), (3, float("inf")), (rot // 2 - 1, float("-inf"))):
+        f[p] = v
+        gone[p] = gone[p + rot // 2] = True
+    got = sas.sas_rotary(x, f.to(DEV)).cpu()
+    kc, vc = (torch.zeros((1, 2, 128, d), dtype=x.dtype, device=DEV) for _ in range(2))
+    sas.sas_cache_append(x, x, i32([0]), kc, vc, inv_freq=f.to(DEV))
+    for y in (got, kc[:, :, :N].cpu()):
+        assert torch.isnan(y[..., gone]).all()
+        assert torch.equal(y[..., ~gone], want.cpu()[..., ~gone])
+    assert torch.equal(vc[:, :, :N], x)
+
+
 # ---------------------------------------------------------------- page tables
 def page_case(seed, B, T, top, width=None, short=0):
     rng = np.random.Generator(np.random.PCG64(seed))
