@@ -58,6 +58,9 @@ sas_status sas_rotary(const void* q, const int64_t* q_strides, void* qo,
   REQUIRE(inverse == 0 || inverse == 1, SAS_ERR_INVALID_ARG, "inverse must be 0 or 1");
   REQUIRE(pos == nullptr || (start == nullptr && parents == nullptr), SAS_ERR_INVALID_ARG,
           "pos excludes start and parents");
+  // every thread walks its token's ancestors, so a long chain costs N squared
+  REQUIRE(parents == nullptr || N <= 1024, SAS_ERR_UNSUPPORTED,
+          "N must be <= 1024 with parents (got %d)", N);
   if (B == 0 || N == 0) return SAS_OK;
   s = check_rotation(inv_freq, rot, d, interleaved, amplitude);
   if (s != SAS_OK) return s;

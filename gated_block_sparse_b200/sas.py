@@ -515,7 +515,7 @@ def sas_rotary(q, inv_freq, k=None, pos=None, start=None, parents=None, interlea
     q and k may be strided views (a fused projection's) with contiguous rows.
     inv_freq [rot/2] fp32 sets the frequencies and the rotated width; the
     positions are pos [B][N], or start [B] (0 if None) plus the token's index,
-    or plus its depth in the tree of parents [B][N]. inverse=True is the
+    or plus its depth in the tree of parents [B][N <= 1024]. inverse=True is the
     transpose: it takes the gradients of the outputs to those of the inputs.
     out: qo, or (qo, ko); q and k themselves rotate in place.
     """

@@ -53,7 +53,8 @@ extern "C" {
  *     (start [B] int32, NULL = 0) + n, or + the depth of token n when
  *     parents [B][N] int32 is given (the tree of sas_decode_tree: a parent is
  *     below its child, -1 has depth 0; another entry is reported and read
- *     as -1)
+ *     as -1; N <= 1024 then, since every token walks up its path). Positions
+ *     are int32: start + n has to stay below 2^31
  *   d in {64, 128}; B <= 65535
  */
 sas_status sas_rotary(const void* q, const int64_t* q_strides, void* qo,

@@ -216,6 +216,20 @@ def test_rotary_of_frequencies_that_are_not_finite(dtype, rot):
     assert torch.equal(vc[:, :, :N], x)
 
 
+@pytest.mark.parametrize("N", [65, 1024])
+def test_rotary_of_long_trees(N):
+    """The longest tree that is taken: a chain, and a random tree beside it."""
+    f = rope.inv_freq(64)[0].to(DEV)
+    par = np.stack([np.arange(N) - 1, S.parents_of("tree", 1, N, np.random.Generator(
+        np.random.PCG64(N)))[0]]).astype(np.int32)
+    q = torch.randn((2, 3, N, 64), generator=torch.Generator().manual_seed(N)).to(DEV)
+    got = sas.sas_rotary(q, f, start=i32([5, 900]), parents=i32(par))
+    want = sas.sas_rotary(q, f, pos=i32(np.array([[5], [900]]) + SO.depths(par)))
+    assert torch.equal(got, want)
+    with pytest.raises(sas.SasError, match="1024 with parents"):
+        sas.sas_rotary(q[:, :, :1].expand(2, 3, 1025, 64), f, parents=i32(np.full((2, 1025), -1)))
+
+
 # ---------------------------------------------------------------- page tables
 def page_case(seed, B, T, top, width=None, short=0):
     rng = np.random.Generator(np.random.PCG64(seed))

@@ -67,6 +67,7 @@ def stride(*s):
     ("sas_rotary", ROTARY, dict(inverse=3), 1, b"inverse"),
     ("sas_rotary", ROTARY, dict(pos=FAKE, start=FAKE), 1, b"excludes"),
     ("sas_rotary", ROTARY, dict(start=FAKE + 4), 1, b"start"),
+    ("sas_rotary", ROTARY, dict(parents=FAKE, N=1025), 2, b"1024 with parents"),
     ("sas_rotary", ROTARY, dict(B=70000), 2, b"65535"),
     ("sas_rotary", ROTARY, dict(qs=stride(0, -128, 128)), 1, b"input strides"),
     ("sas_rotary", ROTARY, dict(kos=stride(2048, 1024, 64)), 1, b"output strides"),
