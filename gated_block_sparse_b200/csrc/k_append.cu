@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(AP_THREADS, 2) k_append(AppendArgs a) {
       }
       if (a.slots) {
         slot = a.slots[(size_t)b * a.T + j];
-        if (slot >= 0 && (slot >> 6) >= a.npages) {
+        if (slot < -1 || (slot >= 0 && (slot >> 6) >= a.npages)) {
           atomicOr(&g_append_err, kErrBadIndex);
           slot = -1;
         }

@@ -113,8 +113,8 @@ sas_status sas_page_map(const int32_t* lens, const int32_t* nnew, int32_t* block
  *   lens [B], the lengths before; ntok [B] or NULL (T everywhere); rows [B][T]
  *     or NULL (a row may be named twice). q needs inv_freq and no rows.
  *   N a multiple of 64 (0 with slots). A token past N, a row outside [0, T)
- *     or a page outside [0, npages) is left out and reported, as is a
- *     sequence with lens < 0 or ntok outside [0, T].
+ *     or a slot below -1 or in a page past npages is left out and reported, as
+ *     is a sequence with lens < 0 or ntok outside [0, T] (its rows of qo too).
  * Slots of two tokens must differ. No workspace.
  */
 sas_status sas_cache_append(const void* q, const int64_t* q_strides, void* qo, const void* k,

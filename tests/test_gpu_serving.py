@@ -413,6 +413,22 @@ def test_cache_append_leaves_out_what_is_out_of_range():
     assert torch.equal(vc[:, :, 60:], x["v"][:, :, :4])
 
 
+@pytest.mark.parametrize("slot,reported", [(-1, False), (-2, True), (-64, True), (-2 ** 31, True)])
+def test_cache_append_reports_slots_below_minus_one(slot, reported):
+    c = ("bf16", "f32", 1, 2, 2, 70, 64, [0], [70], True, 0, False, False, False)
+    x = append_case(c)
+    kc0 = x["kc"].clone()
+    slots = x["slots"].copy()
+    slots[0, 5] = slot
+    sas.sas_cache_append(x["k"], x["v"], i32([0]), x["kc"], x["vc"], ksum=x["ks"], slots=i32(slots))
+    st, msg = sas.sas_device_status(clear=True)
+    assert (st == 5 and "k_append" in msg) if reported else st == 0
+    slots[0, 5] = -1
+    kc, vc, _ = SO.append(x["k64"], x["v64"], [0], np64(kc0), x["vc64"], x["ks64"], [70], None,
+                          slots, None, lambda y: y, lambda y: y)
+    assert np.array_equal(np64(x["kc"]), kc) and np.array_equal(np64(x["vc"]), vc)
+
+
 # ----------------------------------------------------------------------- tree
 TREE = [  # dtype, sums, B, Hq, Hkv, d, T, N, lens, ntok, topk, gated, kind, paged
     ("f32", "f32", 2, 2, 2, 64, 7, 640, [600, 321], None, 2, 1, "tree", False),
