@@ -134,6 +134,7 @@ sas_status sas_cache_append(const void* q, const int64_t* q_strides, void* qo, c
   REQUIRE((q ? (long long)Hq : 0ll) + Hkv <= 65535, SAS_ERR_UNSUPPORTED, "at most 65535 heads");
   REQUIRE(q == nullptr || (inv_freq != nullptr && rows == nullptr), SAS_ERR_INVALID_ARG,
           "q needs inv_freq and no rows");
+  REQUIRE(T <= (1 << 30), SAS_ERR_UNSUPPORTED, "T must be <= 2^30 (got %d)", T);
   if (slots)
     REQUIRE(npages >= 1 && npages <= (1 << 25), SAS_ERR_INVALID_ARG,
             "npages must be in [1, 2^25] (got %d)", npages);

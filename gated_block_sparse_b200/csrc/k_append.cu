@@ -41,7 +41,8 @@ __global__ void __launch_bounds__(AP_THREADS, 2) k_append(AppendArgs a) {
   const int u = tid % U, g = tid / U;
   const int len = a.lens[b];
   int nt = a.ntok ? a.ntok[b] : a.T;
-  if (len < 0 || nt < 0 || nt > a.T) {  // an impossible count: nothing is appended
+  // an impossible count, or positions past int32: nothing is appended
+  if (len < 0 || nt < 0 || nt > a.T || len > 0x7fffffff - a.T) {
     if (tid == 0 && blockIdx.x == 0 && blockIdx.y == 0) atomicOr(&g_append_err, kErrBadIndex);
     return;
   }

@@ -114,7 +114,8 @@ sas_status sas_page_map(const int32_t* lens, const int32_t* nnew, int32_t* block
  *     or NULL (a row may be named twice). q needs inv_freq and no rows.
  *   N a multiple of 64 (0 with slots). A token past N, a row outside [0, T)
  *     or a slot below -1 or in a page past npages is left out and reported, as
- *     is a sequence with lens < 0 or ntok outside [0, T] (its rows of qo too).
+ *     is a sequence with lens < 0 or ntok outside [0, T] (its rows of qo too),
+ *     or with lens + T past 2^31 - 1. T <= 2^30.
  * Slots of two tokens must differ. No workspace.
  */
 sas_status sas_cache_append(const void* q, const int64_t* q_strides, void* qo, const void* k,

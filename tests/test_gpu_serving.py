@@ -429,6 +429,19 @@ def test_cache_append_reports_slots_below_minus_one(slot, reported):
     assert np.array_equal(np64(x["kc"]), kc) and np.array_equal(np64(x["vc"]), vc)
 
 
+def test_cache_append_reports_positions_past_31_bits():
+    """A length whose tokens would pass the largest int32 position, in a paged
+    cache that does not look at it otherwise: left out; one token less is taken."""
+    c = ("bf16", "f32", 1, 2, 2, 70, 64, [0], [70], True, 64, False, False, False)
+    x = append_case(c)
+    kc0, f = x["kc"].clone(), x["f"].to(DEV)
+    args = (x["kc"], x["vc"])
+    sas.sas_cache_append(x["k"], x["v"], i32([2 ** 31 - 70]), *args, slots=i32(x["slots"]), inv_freq=f)
+    assert sas.sas_device_status(clear=True)[0] == 5 and torch.equal(x["kc"], kc0)
+    sas.sas_cache_append(x["k"], x["v"], i32([2 ** 31 - 71]), *args, slots=i32(x["slots"]), inv_freq=f)
+    assert sas.sas_device_status(clear=True)[0] == 0 and not torch.equal(x["kc"], kc0)
+
+
 # ----------------------------------------------------------------------- tree
 TREE = [  # dtype, sums, B, Hq, Hkv, d, T, N, lens, ntok, topk, gated, kind, paged
     ("f32", "f32", 2, 2, 2, 64, 7, 640, [600, 321], None, 2, 1, "tree", False),

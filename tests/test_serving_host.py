@@ -90,6 +90,8 @@ def stride(*s):
     ("sas_cache_append", APPEND, dict(lens=None), 1, b"lens"),
     ("sas_cache_append", APPEND, dict(vs=stride(1, -1, 1)), 1, b"input strides"),
     ("sas_cache_append", APPEND, dict(kc=FAKE + 2), 1, b"kc"),
+    ("sas_cache_append", APPEND, dict(T=(1 << 30) + 1, ks=stride(0, 128, 0), vs=stride(0, 128, 0)),
+     2, b"2^30"),
     ("sas_decode_tree", TREE, dict(T=65), 2, b"64 drafted"),
     ("sas_decode_tree", TREE, dict(T=0), 1, b"T must be"),
     ("sas_decode_tree", TREE, dict(N=100), 1, b"multiple of 64"),
