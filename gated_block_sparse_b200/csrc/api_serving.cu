@@ -18,6 +18,19 @@ void set_strides(long long (&out)[3], const int64_t* in, int H, int N, int d) {
   out[2] = in ? in[2] : d;
 }
 
+// Whether two ranges of memory share a byte.
+struct Range {
+  uintptr_t lo, hi;
+  Range(const void* p, size_t bytes)
+      : lo(reinterpret_cast<uintptr_t>(p)), hi(reinterpret_cast<uintptr_t>(p) + (p ? bytes : 0)) {}
+  bool meets(const Range& o) const { return lo < o.hi && o.lo < hi; }
+};
+
+// Bytes from the first to behind the last row of a [B][H][N] array of rows of d.
+size_t span_bytes(const long long (&s)[3], int B, int H, int N, int d, int es) {
+  return (size_t)(s[0] * (B - 1) + s[1] * (H - 1) + s[2] * (N - 1) + d) * es;
+}
+
 // Dimensions of one element never use their stride, and no heads use none.
 bool strides_ok(const long long (&s)[3], int B, int H, int N, long long least) {
   if (H == 0) return true;
@@ -167,6 +180,22 @@ sas_status sas_cache_append(const void* q, const int64_t* q_strides, void* qo, c
   REQUIRE(strides_ok(a.ks, B, Hkv, T, 0) && strides_ok(a.vs, B, Hkv, T, 0) &&
               (!q || strides_ok(a.qs, B, Hq, T, 0)),
           SAS_ERR_INVALID_ARG, "input strides must be >= 0");
+  const int es = dt == SAS_BF16 ? 2 : 4;
+  const size_t cache = (slots ? (size_t)npages * 64 : (size_t)B * N) * Hkv * d * es;
+  const Range rk(k, span_bytes(a.ks, B, Hkv, T, d, es)), rv(v, span_bytes(a.vs, B, Hkv, T, d, es));
+  const Range rkc(kc, cache), rvc(vc, cache);
+  REQUIRE(!rkc.meets(rvc), SAS_ERR_INVALID_ARG, "kc and vc must not overlap");
+  REQUIRE(!rk.meets(rkc) && !rk.meets(rvc) && !rv.meets(rkc) && !rv.meets(rvc),
+          SAS_ERR_INVALID_ARG, "k and v must not lie in the cache (blocks are written in any order)");
+  if (q) {
+    const Range rq(q, span_bytes(a.qs, B, Hq, T, d, es)), rqo(qo, (size_t)B * Hq * T * d * es);
+    const bool dense = (B <= 1 || a.qs[0] == (long long)Hq * T * d) &&
+                       (Hq <= 1 || a.qs[1] == (long long)T * d) && (T <= 1 || a.qs[2] == d);
+    REQUIRE((q == qo && dense) || !rq.meets(rqo), SAS_ERR_INVALID_ARG,
+            "qo must be q itself (contiguous) or lie apart from it");
+    REQUIRE(!rqo.meets(rk) && !rqo.meets(rv) && !rqo.meets(rkc) && !rqo.meets(rvc),
+            SAS_ERR_INVALID_ARG, "qo must lie apart from k, v and the cache");
+  }
   a.rows = rows; a.lens = lens; a.ntok = ntok; a.slots = slots;
   a.inv_freq = inv_freq;
   a.amp = amplitude;

@@ -116,7 +116,9 @@ sas_status sas_page_map(const int32_t* lens, const int32_t* nnew, int32_t* block
  *     or a slot below -1 or in a page past npages is left out and reported, as
  *     is a sequence with lens < 0 or ntok outside [0, T] (its rows of qo too),
  *     or with lens + T past 2^31 - 1. T <= 2^30.
- * Slots of two tokens must differ. No workspace.
+ * Slots of two tokens must differ. k and v must not lie in the cache, nor qo in
+ * anything but q (qo = q, contiguous, rotates in place): tokens are moved in any
+ * order. Refused by their addresses. No workspace.
  */
 sas_status sas_cache_append(const void* q, const int64_t* q_strides, void* qo, const void* k,
                             const int64_t* k_strides, const void* v, const int64_t* v_strides,

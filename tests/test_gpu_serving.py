@@ -442,6 +442,31 @@ def test_cache_append_reports_positions_past_31_bits():
     assert sas.sas_device_status(clear=True)[0] == 0 and not torch.equal(x["kc"], kc0)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_cache_append_rotates_q_in_place_and_beside_the_cache(dtype):
+    """qo = q, contiguous; k and v views of a projection that ends where the cache
+    begins; and the refusal of k and v that lie in the cache."""
+    B, Hq, Hkv, T, d, N = 2, 4, 2, 70, 64, 256
+    dt = S.TORCH[dtype]
+    g = torch.Generator().manual_seed(8)
+    n = B * T * 2 * Hkv * d
+    buf = torch.randn(n + 2 * B * Hkv * N * d, generator=g).to(dt).to(DEV)
+    kv = buf[:n].view(B, T, 2 * Hkv, d)
+    k, v = kv[:, :, :Hkv].transpose(1, 2), kv[:, :, Hkv:].transpose(1, 2)
+    kc, vc = buf[n:].view(2, B, Hkv, N, d)
+    q = torch.randn((B, Hq, T, d), generator=g).to(dt).to(DEV)
+    f, lens = rope.inv_freq(d)[0].to(DEV), i32([3, 100])
+    kc2, vc2 = kc.clone(), vc.clone()
+    want = sas.sas_cache_append(k.contiguous(), v.contiguous(), lens, kc2, vc2, inv_freq=f, q=q)
+    assert sas.sas_cache_append(k, v, lens, kc, vc, inv_freq=f, q=q, out=q) is q
+    assert torch.equal(q, want) and torch.equal(kc, kc2) and torch.equal(vc, vc2)
+    for bad in (dict(k=kc[:, :, :T]), dict(v=kc[:, :, N - T:]), dict(k=vc[:, :, 9:9 + T])):
+        with pytest.raises(sas.SasError, match="must not lie in the cache"):
+            sas.sas_cache_append(**{**dict(k=k, v=v), **bad}, lens=lens, kc=kc, vc=vc)
+    with pytest.raises(sas.SasError, match="kc and vc must not overlap"):
+        sas.sas_cache_append(k, v, lens, kc, kc)
+
+
 # ----------------------------------------------------------------------- tree
 TREE = [  # dtype, sums, B, Hq, Hkv, d, T, N, lens, ntok, topk, gated, kind, paged
     ("f32", "f32", 2, 2, 2, 64, 7, 640, [600, 321], None, 2, 1, "tree", False),

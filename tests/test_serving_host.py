@@ -113,6 +113,26 @@ def test_refusals(lib, fn, base, change, status, text):
     assert st == status and text in lib.sas_last_error_message(), lib.sas_last_error_message()
 
 
+@pytest.mark.parametrize("change,text", [
+    # k and v are [1][2][4][128] bf16, 2048 bytes; a cache is [1][2][128][128], 65536
+    (dict(vc=FAKE + (2 << 20)), b"kc and vc"),
+    (dict(vc=FAKE + (2 << 20) + 65520), b"kc and vc"),
+    (dict(k=FAKE + (2 << 20) + 65520), b"k and v must not lie"),
+    (dict(v=FAKE + (3 << 20) - 16), b"k and v must not lie"),
+    (dict(k=FAKE + (2 << 20) - 1008, ks=stride(0, 0, 128)), b"k and v must not lie"),
+    (dict(slots=FAKE, npages=5, N=0, k=FAKE + (2 << 20) + 5 * 32768 - 16), b"k and v must not lie"),
+    (dict(qo=FAKE + (4 << 20) + 16), b"qo must be q itself"),
+    (dict(qo=FAKE + (4 << 20), qs=stride(0, 128, 512)), b"qo must be q itself"),
+    (dict(qo=FAKE + (2 << 20) + 128), b"qo must lie apart"),
+    (dict(qo=FAKE + (5 << 20)), b"qo must lie apart"),
+])
+def test_append_refuses_memory_that_overlaps(lib, change, text):
+    base = dict(APPEND, q=FAKE + (4 << 20), qo=FAKE + (6 << 20), f=FAKE, rot=64,
+                k=FAKE + (1 << 20), v=FAKE + (5 << 20), kc=FAKE + (2 << 20), vc=FAKE + (3 << 20))
+    st = lib.sas_cache_append(*{**base, **change}.values())
+    assert st == 1 and text in lib.sas_last_error_message(), lib.sas_last_error_message()
+
+
 def test_empty_calls_need_no_pointers(lib):
     none = dict.fromkeys(["q", "qo", "k", "ko", "f"], None)
     assert lib.sas_rotary(*{**ROTARY, **none, "Hkv": 0, "B": 0}.values()) == 0
