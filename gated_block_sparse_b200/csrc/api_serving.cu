@@ -2,6 +2,8 @@
 // validation and launches. Host code only.
 #include "../../include/sas_serving.h"
 
+#include <algorithm>
+
 #include "api_common.h"
 #include "kernels.h"
 
@@ -35,6 +37,68 @@ size_t span_bytes(const long long (&s)[3], int B, int H, int N, int d, int es) {
 bool strides_ok(const long long (&s)[3], int B, int H, int N, long long least) {
   if (H == 0) return true;
   return (B <= 1 || s[0] >= least) && (H <= 1 || s[1] >= least) && (N <= 1 || s[2] >= least);
+}
+
+// A [B][H][N] array of rows of d elements: element strides, sizes.
+struct Rows {
+  const void* p;
+  long long s[3];
+  int n[3];
+};
+
+// Whether no two rows of the array share an element: with the strides in
+// ascending order, each passes over the whole extent of the ones before. (Views
+// that torch makes by slicing and transposing are all of that kind.)
+bool rows_apart(const Rows& r, int d) {
+  int order[3] = {0, 1, 2};
+  std::sort(order, order + 3, [&](int i, int j) { return r.s[i] < r.s[j]; });
+  long long extent = d;
+  for (int i : order) {
+    if (r.n[i] <= 1) continue;
+    if (r.s[i] < extent) return false;
+    extent += r.s[i] * (r.n[i] - 1);
+  }
+  return true;
+}
+
+bool same_strides(const Rows& x, const Rows& y) {
+  for (int i = 0; i < 3; ++i)
+    if (x.n[i] > 1 && y.n[i] > 1 && x.s[i] != y.s[i]) return false;
+  return true;
+}
+
+// Whether a row of x shares an element with a row of y (rows_apart holds for y).
+// Equal strides: whether the distance of their first elements is a sum of
+// strides times differences of indices, and less than d; from the largest stride
+// down, two multiples come into question each. Other strides: whether the ranges
+// from first to last row meet.
+bool rows_meet(const Rows& x, const Rows& y, int d, int es) {
+  const Range rx(x.p, span_bytes(x.s, x.n[0], x.n[1], x.n[2], d, es));
+  const Range ry(y.p, span_bytes(y.s, y.n[0], y.n[1], y.n[2], d, es));
+  if (!rx.meets(ry)) return false;
+  if (!same_strides(x, y)) return true;
+  struct Dim {
+    long long s;
+    int lo, hi;  // index of x minus index of y
+  } dim[3];
+  int nd = 0;
+  for (int i = 0; i < 3; ++i)
+    if (x.n[i] > 1 || y.n[i] > 1)
+      dim[nd++] = {x.n[i] > 1 ? x.s[i] : y.s[i], -(y.n[i] - 1), x.n[i] - 1};
+  std::sort(dim, dim + nd, [](const Dim& a, const Dim& b) { return a.s > b.s; });
+  const long long delta = ((long long)ry.lo - (long long)rx.lo) / es;
+  for (int pick = 0; pick < 1 << nd; ++pick) {
+    long long left = delta;
+    bool fits = true;
+    for (int i = 0; i < nd && fits; ++i) {
+      if (dim[i].s <= 0) return true;
+      long long k = left / dim[i].s - (left % dim[i].s < 0) + (pick >> i & 1);
+      fits = k >= dim[i].lo && k <= dim[i].hi;
+      left -= k * dim[i].s;
+    }
+    if (fits && left > -d && left < d) return true;
+  }
+  return false;
 }
 
 sas_status check_rotation(const float* inv_freq, int rot, int d, int interleaved,
@@ -95,6 +159,22 @@ sas_status sas_rotary(const void* q, const int64_t* q_strides, void* qo,
           "input strides must be >= 0");
   REQUIRE(strides_ok(tq.ys, B, Hq, N, d) && strides_ok(tk.ys, B, Hkv, N, d), SAS_ERR_INVALID_ARG,
           "output strides must be >= d (rows must not overlap)");
+  const int es = dt == SAS_BF16 ? 2 : 4;
+  auto rows = [&](const void* p, const long long (&st)[3], int H) {
+    return Rows{p, {st[0], st[1], st[2]}, {B, H, N}};
+  };
+  const Rows in[2] = {rows(q, tq.xs, Hq), rows(k, tk.xs, Hkv)};
+  const Rows out[2] = {rows(qo, tq.ys, Hq), rows(ko, tk.ys, Hkv)};
+  for (int j = 0; j < (k ? 2 : 1); ++j)
+    REQUIRE(rows_apart(out[j], d), SAS_ERR_INVALID_ARG, "output rows must not overlap");
+  REQUIRE(!k || !rows_meet(out[0], out[1], d, es), SAS_ERR_INVALID_ARG,
+          "qo and ko must not overlap");
+  for (int i = 0; i < (k ? 2 : 1); ++i)
+    for (int j = 0; j < (k ? 2 : 1); ++j) {
+      const bool in_place = i == j && in[i].p == out[j].p && same_strides(in[i], out[j]);
+      REQUIRE(in_place || !rows_meet(in[i], out[j], d, es), SAS_ERR_INVALID_ARG,
+              "an output must be its input itself, with its strides, or lie apart from the inputs");
+    }
   return cuda_status(sas::launch_rotary(tq, tk, dt == SAS_BF16, B, N, d, inv_freq, rot,
                                         interleaved, amplitude, inverse, pos, start, parents,
                                         (cudaStream_t)stream),

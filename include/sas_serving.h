@@ -46,7 +46,9 @@ extern "C" {
  *     through element strides {batch, head, token}; qo, ko likewise. A stride
  *     pointer (host memory, three values) of NULL means contiguous. Rows of d
  *     elements are contiguous. Input strides may be 0 (shared rows), output
- *     rows must not overlap; qo = q with equal strides rotates in place.
+ *     rows must not overlap; qo = q with equal strides rotates in place, any
+ *     other overlap of an output with an input or with the other output is
+ *     refused (by address; rows of one buffer may alternate if strides agree).
  *   inv_freq [rot/2] fp32, radians per position (an entry that is not finite
  *     turns its pair to NaN); rot even, 2 <= rot <= d
  *   pos [B][N] int32: the positions; or NULL, then position = start[b]

@@ -230,6 +230,33 @@ def test_rotary_of_long_trees(N):
         sas.sas_rotary(q[:, :, :1].expand(2, 3, 1025, 64), f, parents=i32(np.full((2, 1025), -1)))
 
 
+@pytest.mark.parametrize("N,Hkv", [(1, 2), (5, 1), (70, 2)])
+def test_rotary_within_one_buffer(N, Hkv):
+    """Inputs and outputs that alternate in one buffer without sharing a row are
+    taken; a view shifted by a head or a token is refused."""
+    B, Hq, d = 2, 4, 64
+    g = torch.Generator().manual_seed(N)
+    f, H = rope.inv_freq(d)[0].to(DEV), Hq + Hkv
+    x = torch.randn((B, N, 2, H + 1, d), generator=g).bfloat16().to(DEV)
+    keep = x.clone()
+    heads = lambda t, lo, n: t[:, :, :, lo:lo + n].permute(2, 0, 3, 1, 4)  # [2][B][H][N][d]
+    (q, qo), (k, ko) = heads(x, 0, Hq), heads(x, Hq, Hkv)
+    want = sas.sas_rotary(q.contiguous(), f, k=k.contiguous())
+    sas.sas_rotary(q, f, k=k, out=(qo, ko))
+    assert torch.equal(qo, want[0]) and torch.equal(ko, want[1])
+    assert torch.equal(x[:, :, 0], keep[:, :, 0]) and torch.equal(x[:, :, 1, H], keep[:, :, 1, H])
+    with pytest.raises(sas.SasError, match="an output must be"):
+        sas.sas_rotary(q, f, k=k, out=(heads(x, 1, Hq)[0], ko))
+    with pytest.raises(sas.SasError, match="qo and ko"):
+        sas.sas_rotary(q, f, k=k, out=(qo, heads(x, Hq - 1, Hkv)[1]))
+    if N > 2:
+        with pytest.raises(sas.SasError, match="an output must be"):
+            sas.sas_rotary(q[:, :, 1:], f, out=q[:, :, :-1])
+    sas.sas_rotary(q, f, k=k, out=(q, k))  # in place
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1])
+    assert torch.equal(x[:, :, 0, H], keep[:, :, 0, H])
+
+
 # ---------------------------------------------------------------- page tables
 def page_case(seed, B, T, top, width=None, short=0):
     rng = np.random.Generator(np.random.PCG64(seed))

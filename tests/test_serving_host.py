@@ -114,6 +114,29 @@ def test_refusals(lib, fn, base, change, status, text):
 
 
 @pytest.mark.parametrize("change,text", [
+    # B 2, N 8, d 128, bf16: contiguous q [2][4][8][128], 16384 bytes; k half of it
+    (dict(qos=stride(4096, 128, 128)), b"output rows must not overlap"),
+    (dict(qos=stride(1024, 1024, 128)), b"output rows must not overlap"),
+    (dict(kos=stride(2048, 1024, 1024)), b"output rows must not overlap"),
+    (dict(ko=FAKE + (2 << 20) + 16384 - 16), b"qo and ko"),
+    (dict(qo=FAKE + (1 << 20), qos=stride(4096, 128, 512)), b"an output must be"),
+    (dict(qo=FAKE + (1 << 20) + 256), b"an output must be"),
+    (dict(qo=FAKE + (1 << 20) - 16368), b"an output must be"),
+    (dict(qo=FAKE + (3 << 20)), b"an output must be"),  # k
+    # views of one buffer [2][8][6 heads][128]: k's heads into q's, or a token ahead
+    (dict(qs=stride(6144, 128, 768), ks=stride(6144, 128, 768), k=FAKE + (1 << 20) + 1024,
+          kos=stride(6144, 128, 768), ko=FAKE + (1 << 20) + 768), b"an output must be"),
+    (dict(qs=stride(6144, 128, 768), qo=FAKE + (1 << 20) + 1536, qos=stride(6144, 128, 768)),
+     b"an output must be"),
+])
+def test_rotary_refuses_memory_that_overlaps(lib, change, text):
+    base = dict(ROTARY, B=2, q=FAKE + (1 << 20), qo=FAKE + (2 << 20), k=FAKE + (3 << 20),
+                ko=FAKE + (4 << 20))
+    st = lib.sas_rotary(*{**base, **change}.values())
+    assert st == 1 and text in lib.sas_last_error_message(), lib.sas_last_error_message()
+
+
+@pytest.mark.parametrize("change,text", [
     # k and v are [1][2][4][128] bf16, 2048 bytes; a cache is [1][2][128][128], 65536
     (dict(vc=FAKE + (2 << 20)), b"kc and vc"),
     (dict(vc=FAKE + (2 << 20) + 65520), b"kc and vc"),
