@@ -206,6 +206,26 @@ sas_status sas_page_map(const int32_t* lens, const int32_t* nnew, int32_t* block
   if (nfree > 0) REQUIRE_PTR(free_pages);
   REQUIRE_PTR(free_head);
   REQUIRE_PTR(head_out);
+  // every array apart from the ones that are written, but for the two in place
+  const struct {
+    const char* name;
+    Range r;
+  } arrays[] = {{"slots", {slots, (size_t)B * T * 4}},
+                {"new_lens", {new_lens, (size_t)B * 4}},
+                {"taken", {taken, (size_t)B * 4}},
+                {"head_out", {head_out, 4}},
+                {"block_table", {block_table, (size_t)B * width * 4}},
+                {"lens", {lens, (size_t)B * 4}},
+                {"nnew", {nnew, (size_t)B * 4}},
+                {"free_pages", {free_pages, (size_t)nfree * 4}},
+                {"free_head", {free_head, 4}}};
+  for (int i = 0; i < 5; ++i)
+    for (int j = i + 1; j < 9; ++j) {
+      const bool in_place = (i == 1 && j == 5 && new_lens == lens) ||
+                            (i == 3 && j == 8 && head_out == free_head);
+      REQUIRE(in_place || !arrays[i].r.meets(arrays[j].r), SAS_ERR_INVALID_ARG,
+              "%s and %s must not overlap", arrays[i].name, arrays[j].name);
+    }
   const sas::PageMapArgs a{lens,  nnew,     block_table, free_pages, free_head, slots, new_lens,
                            taken, head_out, B,           T,          width,     npages, nfree};
   return cuda_status(sas::launch_page_map(a, (cudaStream_t)stream), "sas_page_map launch");

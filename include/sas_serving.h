@@ -87,7 +87,9 @@ sas_status sas_rotary(const void* q, const int64_t* q_strides, void* qo,
  * counts, so the order decides) or when its numbers are impossible (negative,
  * nnew > T, more than 64 width tokens). A page id outside [0, npages) is
  * written as listed, gives slots of -1 and is reported.
- *   npages <= 2^25; B <= 65534, B (T + 128) < 2^31. No workspace.
+ *   npages <= 2^25; B <= 65534, B (T + 128) < 2^31. No workspace. No array that
+ *   is written may overlap another, but for new_lens = lens and head_out =
+ *   free_head (checked).
  */
 sas_status sas_page_map(const int32_t* lens, const int32_t* nnew, int32_t* block_table,
                         const int32_t* free_pages, const int32_t* free_head, int B, int T,

@@ -156,6 +156,29 @@ def test_append_refuses_memory_that_overlaps(lib, change, text):
     assert st == 1 and text in lib.sas_last_error_message(), lib.sas_last_error_message()
 
 
+@pytest.mark.parametrize("change,text", [
+    # B 2, T 4, width 3, nfree 4: slots 32 bytes, table 24, free list 16, the rest 8 and 4
+    (dict(new="nnew"), b"new_lens and nnew"),
+    (dict(new=0x20000 + 0), b"new_lens and slots"),
+    (dict(taken="lens"), b"taken and lens"),
+    (dict(taken="new"), b"new_lens and taken"),
+    (dict(out="taken"), b"taken and head_out"),
+    (dict(slots="free"), b"slots and free_pages"),
+    (dict(slots=0x60000 - 16), b"slots and free_pages"),
+    (dict(table=0x50000 - 16), b"block_table and nnew"),
+    (dict(out="free"), b"head_out and free_pages"),
+    (dict(new=0x40000 + 0, out="head", taken=0x70000), b"taken and head_out"),
+])
+def test_page_map_refuses_memory_that_overlaps(lib, change, text):
+    base = dict(PAGES, slots=0x20000, table=0x30000, lens=0x40000, nnew=0x50000, free=0x60000,
+                head=0x70000, new=0x80000, taken=0x90000, out=0xA0000)
+    change = {k: base[v] if isinstance(v, str) else v for k, v in change.items()}
+    st = lib.sas_page_map(*{**base, **change}.values())
+    names = text.split(b" and ")
+    assert st == 1 and all(n in lib.sas_last_error_message() for n in names), \
+        lib.sas_last_error_message()
+
+
 def test_empty_calls_need_no_pointers(lib):
     none = dict.fromkeys(["q", "qo", "k", "ko", "f"], None)
     assert lib.sas_rotary(*{**ROTARY, **none, "Hkv": 0, "B": 0}.values()) == 0
