@@ -146,9 +146,11 @@ struct Place {
   }
 };
 
-// Outputs of one call, carved from one allocation (an allocation of its own
-// costs 0.9 us, as much as the call's checks): contiguous tensors that share a
-// storage, each from a 16-byte boundary.
+// Outputs of one call. Those below `limit` bytes are carved from one allocation
+// (an allocation of its own costs 0.9 us, as much as the call's checks):
+// contiguous tensors that share a storage, each from a 16-byte boundary, so that
+// one of them that is kept holds less than N limit bytes. Larger ones have
+// a storage of their own.
 template <int N>
 struct Outputs {
   int64_t elems = 0, at[N];
@@ -160,20 +162,25 @@ struct Outputs {
     return (n + per16 - 1) / per16 * per16;
   }
   void make(const Place& pl, at::ScalarType dt, const at::IntArrayRef (&shapes)[N],
-            const bool (&wanted)[N]) {
-    const int64_t per16 = 16 / (int64_t)c10::elementSize(dt);
+            const bool (&wanted)[N], int64_t limit) {
+    const int64_t es = (int64_t)c10::elementSize(dt), per16 = 16 / es;
     int count = 0;
     for (int i = 0; i < N; ++i) {
-      at[i] = elems;
-      if (wanted[i]) {
-        elems += padded(shapes[i], per16);
-        ++count;
+      at[i] = -1;
+      if (!wanted[i]) continue;
+      const int64_t n = padded(shapes[i], per16);
+      if (n * es >= limit) {
+        t[i] = pl.empty(shapes[i], dt);
+        continue;
       }
+      at[i] = elems;
+      elems += n;
+      ++count;
     }
     if (count == 0) return;
     const at::Tensor base = pl.empty({elems}, dt);
     for (int i = 0; i < N; ++i) {
-      if (!wanted[i]) continue;
+      if (at[i] < 0) continue;
       t[i] = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(base.storage()), base.key_set(),
                                                       base.dtype());
       t[i].unsafeGetTensorImpl()->set_storage_offset(at[i]);
@@ -250,7 +257,7 @@ PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t Hkv = k ? size_of(*k, "k", 4, 1) : 0, half = f.numel();
     const int64_t qshape[4] = {B, Hq, N, d}, kshape[4] = {B, Hkv, N, d};
     Outputs<2> made;
-    made.make(pl, st, {qshape, kshape}, {!qo, k && !ko});
+    made.make(pl, st, {qshape, kshape}, {!qo, k && !ko}, 1 << 20);  // used and dropped together
     if (!qo) qo = &made.t[0];
     if (k && !ko) ko = &made.t[1];
     int64_t s[4][3];
@@ -289,7 +296,8 @@ PyObject* page_map(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                 tensor(a[9], "taken"), tensor(a[10], "head")};
     const int64_t s0[2] = {B, T}, s1[1] = {B}, s3[1] = {1};
     Outputs<4> made;
-    made.make(pl, at::kInt, {s0, s1, s1, s3}, {!out[0], !out[1], !out[2], !out[3]});
+    // a loop keeps lengths and head, not slots
+    made.make(pl, at::kInt, {s0, s1, s1, s3}, {!out[0], !out[1], !out[2], !out[3]}, 4096);
     for (int i = 0; i < 4; ++i)
       if (!out[i]) out[i] = &made.t[i];
     check_status("sas_page_map",

@@ -955,6 +955,30 @@ def test_outputs_of_a_call_are_ordinary_tensors():
     assert out[0].tolist() == [[3, -1, -1], [-1] * 3, [5 * 64 + 6, 5 * 64 + 7, -1]]
 
 
+def test_kept_outputs_do_not_hold_large_ones():
+    """The head or the lengths of a page map, or one tensor of a rotation, kept
+    after a large call: memory of the others is free again."""
+    def held(make):
+        torch.cuda.synchronize()
+        before = torch.cuda.memory_allocated()
+        keep = make()
+        torch.cuda.synchronize()
+        return torch.cuda.memory_allocated() - before, keep
+    B, T = 64, 8192
+    z = i32(np.zeros(B))
+    args = (z, z, i32(np.zeros((B, 1))), i32([0]), i32([0]), T, 8)
+    for i, most in ((1, 4 * 4096), (2, 4 * 4096), (3, 4 * 4096), (0, 4 * B * T + 512)):
+        n, keep = held(lambda: sas.sas_page_map(*args)[i])
+        assert n <= most and keep.untyped_storage().nbytes() <= most
+    n, keep = held(lambda: sas.sas_page_map(z[:4], z[:4], i32(np.zeros((4, 1))), *args[3:5], 9, 8)[3])
+    assert n <= 4 * 4096
+    f = rope.inv_freq(128)[0].to(DEV)
+    x = torch.zeros((1, 10, 4096, 128), dtype=torch.bfloat16, device=DEV)
+    for i, H in ((0, 8), (1, 2)):
+        n, keep = held(lambda: sas.sas_rotary(x[:, :8], f, k=x[:, 8:])[i])
+        assert n <= H * 4096 * 256 + 512 and keep.untyped_storage().nbytes() == H * 4096 * 256
+
+
 # ------------------------------------------------------------ streams, graphs
 def test_calls_on_another_stream_and_in_graphs():
     B, Hq, Hkv, d, T, N, topk = 2, 4, 2, 128, 6, 1024, 4
