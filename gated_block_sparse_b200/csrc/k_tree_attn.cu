@@ -12,10 +12,10 @@
 // registers. fp32 FMAs bound it: the copy of a unit's keys runs under the
 // softmax and P V of the unit before, that of its values under Q K and the
 // softmax, in one buffer each (at d 128 a second pair would halve the CTAs
-// of an SM). Against both copied before the unit's arithmetic: 16K cache, 24
-// tokens, 32/8 heads, top-k 31 (d 128) 104.6 -> 97.0 us a call; 2 x 3000, 20
-// tokens, 8/2 heads 51.2 -> 48.2; 8 tokens at 8000 25.7 -> 25.0; splits of
-// one unit each are unchanged.
+// of an SM). Against both copied before the unit's arithmetic, us a call at d
+// 128, top-k 31, random trees, contiguous: one sequence of 16300, 32/8 heads, 24
+// tokens 104.3 -> 96.4; two of 3000, 8/2 heads, 20 tokens 50.6 -> 47.7; one of
+// 8000, 32/8 heads, 8 tokens 68.5 -> 64.5; splits of one unit each are unchanged.
 #include <math.h>
 
 #include "common.cuh"

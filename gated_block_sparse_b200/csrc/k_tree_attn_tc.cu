@@ -30,10 +30,11 @@
 // the rounding of the output alone. Everything else is fp32.
 // About 100 KB of shared memory and 256 TMEM columns, so two CTAs an SM. In the
 // loop a CTA takes 1.5 us a unit, 5.7 TB/s over all CTAs: HBM bounds 8 x 128K
-// (125 MB of kept blocks, 33 us with the start, the last CTAs of uneven groups
+// (125 MB of kept blocks, 42 us with the start, the last CTAs of uneven groups
 // and the partial outputs), L2's way to the SMs 512K with T = 64 (two tiles of
-// rows read the same 36 MB, 20 us). 64K, T = 4: 7 us, latencies. An L2 prefetch
-// of the units ahead cost 5% instead (it delays the first loads).
+// rows read the same 36 MB, 30 us). 64K, T = 4: 12 us, latencies. (ncu, the kernel
+// alone; in a call its start overlaps the selection.) An L2 prefetch of the units
+// ahead cost 5% instead (it delays the first loads).
 #include <cuda.h>
 #include <math.h>
 

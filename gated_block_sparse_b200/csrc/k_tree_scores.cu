@@ -20,10 +20,13 @@
 // anywhere), split them and store the parts as swizzled K-major tiles; one
 // thread issues the MMAs; four warps read a token's scores of 32 consecutive
 // blocks from TMEM and write them, 128 bytes a store. Every summary is read
-// once. 512K, T = 64: 34 MB read, 17 MB of scores written, 17 us, where the reads
-// take 5, the writes 3 and the MMAs 3: a CTA's loads, splits, MMAs and stores
-// follow one another, and two CTAs an SM overlap them in part. 8 x 128K, T = 16,
-// bf16 summaries: 29 MB in 13 us. 64K, T = 4: 4 us, a chain of latencies.
+// once. 512K, T = 64: 34 MB read, 17 MB of scores written in 19.5 us (ncu, the
+// kernel alone, 2 us of it its start), where the reads take 5, the writes 3 and
+// the MMAs 3: a CTA's loads, splits, MMAs and stores follow one another. 8 x
+// 128K, T = 16, bf16 summaries, two CTAs an SM: 29 MB in 15 us. 64K, T = 4: 6 us,
+// a chain of latencies. fp32 summaries of d = 128 in two steps of 64 columns, so
+// that two CTAs share an SM: 512K, T = 64 65.0 us a call against 65.3 in one
+// step, 8 x 128K, T = 16 81.2 against 82.5, but 512K, T = 4 32.7 against 29.5.
 #include <math.h>
 
 #include "common.cuh"
@@ -111,23 +114,22 @@ __device__ __noinline__ float score_by_fma(const S* sum, const unsigned char* sb
   return dot;
 }
 
-// CTAs an SM: the 64 fp32 values that a thread loads ahead with STEP = 128 need
+// CTAs an SM: the 64 fp32 values that a thread loads ahead with D = 128 need
 // more than the 128 registers of two (a spilled one would be waited for).
-template <typename S, int STEP>
-constexpr int scores_ctas() { return sizeof(S) * STEP > 256 ? 1 : 2; }
+template <typename S, int D>
+constexpr int scores_ctas() { return sizeof(S) * D > 256 ? 1 : 2; }
 
 __host__ __device__ __forceinline__ int scores_cols(int T) { return (T + 15) & ~15; }
 
 }  // namespace
 
-// STEP: columns of a tile that are in shared memory at a time (64 or D).
-template <typename T, typename S, int D, int STEP>
-__global__ void __launch_bounds__(SC_THREADS, scores_ctas<S, STEP>()) k_tree_scores(TreeArgs a, TreeWs w, int stretch) {
+template <typename T, typename S, int D>
+__global__ void __launch_bounds__(SC_THREADS, scores_ctas<S, D>()) k_tree_scores(TreeArgs a, TreeWs w, int stretch) {
   constexpr int NP = sizeof(S) == 4 ? 3 : 1;     // parts of a summary
   constexpr int PC = D / 8;                      // 16-byte pieces of a bf16 row
-  constexpr int SP = STEP / 8, PER = SC_ROWS * SP / SC_THREADS;  // pieces of a step, of a thread
+  constexpr int PER = SC_ROWS * PC / SC_THREADS; // pieces of a tile of a thread
   constexpr int BI = TREE_MAX * PC / SC_THREADS;
-  constexpr uint32_t A_PART = SC_ROWS * STEP * 2;
+  constexpr uint32_t A_PART = SC_ROWS * D * 2;
   constexpr int VT = Vec16<T>::N;
   extern __shared__ __align__(1024) unsigned char sm[];  // parts of A, then parts of B
   __shared__ uint64_t bar;
@@ -162,7 +164,8 @@ __global__ void __launch_bounds__(SC_THREADS, scores_ctas<S, STEP>()) k_tree_sco
     // wait for them and they for it.
     if (lane == 0) grid_dep_launch();
   }
-  // Rows of a step, a step ahead; where they lie (row or page), a tile ahead. A row past the end reads the last one.
+  // Rows of a tile, a tile ahead; where they lie (row or page), one more. A row
+  // past the end reads the last one.
   Raw8<S> x[PER];
   int at[PER];
   // A page outside the pool gives NaN scores, which the read-out turns to -inf.
@@ -173,21 +176,20 @@ __global__ void __launch_bounds__(SC_THREADS, scores_ctas<S, STEP>()) k_tree_sco
   auto place_tile = [&](int m0) {
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-      at[i] = place_of(min(m0 + tid / SP + i * (SC_THREADS / SP), m_hi - 1));
+      at[i] = place_of(min(m0 + tid / PC + i * (SC_THREADS / PC), m_hi - 1));
   };
-  auto load_step = [&](int step) {
+  auto load_tile = [&] {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       if (tree_page_ok(a, at[i]))
-        x[i].load(static_cast<const S*>(a.ksum) + sum_row(at[i]) * D + step * STEP +
-                  (tid % SP) * 8);
+        x[i].load(static_cast<const S*>(a.ksum) + sum_row(at[i]) * D + (tid % PC) * 8);
       else
         x[i].nan();
     }
   };
   place_tile(m_lo);
   // B: qbar in three parts side by side, zeros behind the last token; its loads
-  // first, then those of the first half of A, then the parts
+  // first, then those of the first tile of A, then the parts
   float s[BI][8];
 #pragma unroll
   for (int e = 0; e < BI; ++e) {
@@ -208,8 +210,8 @@ __global__ void __launch_bounds__(SC_THREADS, scores_ctas<S, STEP>()) k_tree_sco
       }
     }
   }
-  load_step(0);
-  if (D == STEP) place_tile(m_lo + SC_ROWS);
+  load_tile();
+  place_tile(m_lo + SC_ROWS);
   const float inv_g = 1.0f / (float)G;
 #pragma unroll
   for (int e = 0; e < BI; ++e) {
@@ -230,54 +232,43 @@ __global__ void __launch_bounds__(SC_THREADS, scores_ctas<S, STEP>()) k_tree_sco
   uint32_t tmem = 0;
   uint32_t phase = 0;
   for (int m0 = m_lo; m0 < m_hi; m0 += SC_ROWS) {
-#pragma unroll 1
-    for (int step = 0; step < D / STEP; ++step) {
-      // the previous step's MMAs are done (waited on below), so A is free
+    // the previous tile's MMAs are done (waited on below), so A is free
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        uint4 part[NP];
-        x[i].parts(part);
+    for (int i = 0; i < PER; ++i) {
+      uint4 part[NP];
+      x[i].parts(part);
 #pragma unroll
-        for (int k = 0; k < NP; ++k)
-          *reinterpret_cast<uint4*>(sm + k * A_PART +
-                                    sw_off(tid / SP + i * (SC_THREADS / SP), tid % SP, SC_ROWS)) =
-              part[k];
-      }
-      fence_proxy_async_smem();  // A and B are read by the tensor cores
-      tc::fence_before_sync();   // and the previous tile's scores have been read
-      __syncthreads();
-      tc::fence_after_sync();
-      tmem = tmem_slot;
-      if (tid == 0) {
-#pragma unroll 1
-        for (int k = 0; k < NP; ++k) {
-          const uint32_t idesc = tc::idesc_bf16(128, (3 - k) * NT, 0, 0);
-          // a step along K moves a descriptor's address field (16-byte units) alone
-          const uint64_t ad = a_desc + ((k * A_PART) >> 4);
-          const uint32_t chunk = (uint32_t)(3 * NT) * 128;  // 64 columns of B
-          const uint64_t bd = b_desc + ((step * (STEP / 64) * chunk) >> 4);
-#pragma unroll
-          for (int ks = 0; ks < STEP / 16; ++ks) {  // K in steps of 16 (32 bytes)
-            const uint32_t c = ks >> 2, off = (ks & 3) * 32;
-            tc::mma_bf16(tmem, ad + ((c * (SC_ROWS * 128) + off) >> 4),
-                         bd + ((c * chunk + off) >> 4), idesc,
-                         (step > 0 || k > 0 || ks > 0) ? 1u : 0u);
-          }
-        }
-        tc::commit(&bar);
-      }
-      // the next step's rows; the next tile's places once this one's are used
-      if (step + 1 < D / STEP)
-        load_step(step + 1);
-      else if (m0 + SC_ROWS < m_hi)
-        load_step(0);
-      if (step + 2 == D / STEP)
-        place_tile(m0 + SC_ROWS);
-      else if (D == STEP)
-        place_tile(m0 + 2 * SC_ROWS);
-      mbar_wait_data(&bar, phase, err);
-      phase ^= 1;
+      for (int k = 0; k < NP; ++k)
+        *reinterpret_cast<uint4*>(sm + k * A_PART +
+                                  sw_off(tid / PC + i * (SC_THREADS / PC), tid % PC, SC_ROWS)) =
+            part[k];
     }
+    fence_proxy_async_smem();  // A and B are read by the tensor cores
+    tc::fence_before_sync();   // and the previous tile's scores have been read
+    __syncthreads();
+    tc::fence_after_sync();
+    tmem = tmem_slot;
+    if (tid == 0) {
+#pragma unroll 1
+      for (int k = 0; k < NP; ++k) {
+        const uint32_t idesc = tc::idesc_bf16(128, (3 - k) * NT, 0, 0);
+        // a step along K moves a descriptor's address field (16-byte units) alone
+        const uint64_t ad = a_desc + ((k * A_PART) >> 4);
+        const uint32_t chunk = (uint32_t)(3 * NT) * 128;  // 64 columns of B
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {  // K in steps of 16 (32 bytes)
+          const uint32_t c = ks >> 2, off = (ks & 3) * 32;
+          tc::mma_bf16(tmem, ad + ((c * (SC_ROWS * 128) + off) >> 4),
+                       b_desc + ((c * chunk + off) >> 4), idesc, (k > 0 || ks > 0) ? 1u : 0u);
+        }
+      }
+      tc::commit(&bar);
+    }
+    // the next tile's rows, and the places of the one after
+    if (m0 + SC_ROWS < m_hi) load_tile();
+    place_tile(m0 + 2 * SC_ROWS);
+    mbar_wait_data(&bar, phase, err);
+    phase ^= 1;
     tc::fence_after_sync();
     // warp w: blocks 32 (w mod 4) .., tokens 32 (w / 4) ..
     const int m = m0 + 32 * (warp & 3) + lane, t0 = 32 * (warp >> 2);
@@ -324,38 +315,23 @@ __global__ void __launch_bounds__(SC_THREADS, scores_ctas<S, STEP>()) k_tree_sco
 }
 
 // ------------------------------------------------------------------ host
-template <typename T, typename S, int D, int STEP>
-static cudaError_t launch_step(const TreeArgs& a, const TreeWs& w, cudaStream_t st) {
+template <typename T, typename S, int D>
+static cudaError_t launch_typed(const TreeArgs& a, const TreeWs& w, cudaStream_t st) {
   const int C = a.N / SAS_BLOCK;
-  const size_t smem = (size_t)(sizeof(S) == 4 ? 3 : 1) * SC_ROWS * STEP * 2 +
+  const size_t smem = (size_t)(sizeof(S) == 4 ? 3 : 1) * SC_ROWS * D * 2 +
                       (size_t)3 * scores_cols(a.T) * D * 2;
-  cudaError_t e = ensure_smem(k_tree_scores<T, S, D, STEP>, smem);
+  cudaError_t e = ensure_smem(k_tree_scores<T, S, D>, smem);
   if (e != cudaSuccess) return e;
   // summaries of a CTA: whole tiles, and one wave of the CTAs that an SM holds
   const long long groups = (long long)a.B * a.Hkv;
-  const long long room = 148 * scores_ctas<S, STEP>();
+  const long long room = 148 * scores_ctas<S, D>();
   long long per_group = room / groups;
   if (per_group < 1) per_group = 1;
   long long stretch = (C + per_group - 1) / per_group;
   stretch = (stretch + SC_ROWS - 1) / SC_ROWS * SC_ROWS;
-  return tree_launch(k_tree_scores<T, S, D, STEP>,
+  return tree_launch(k_tree_scores<T, S, D>,
                      dim3((unsigned)((C + stretch - 1) / stretch), a.Hkv, a.B), SC_THREADS, smem,
                      st, a, w, (int)stretch);
-}
-
-// Two steps of 64 columns let two CTAs of fp32 summaries at d = 128 share an SM,
-// one splitting while the other's MMAs run (512K, 64 tokens: 17 us in one step
-// of one CTA, 13 in two). Where every CTA has one tile, as in a single 64K
-// sequence, one step is shorter (the step's 23 us become 24 with two), and
-// bf16 summaries need no splitting (8 x 128K: 61 us, and 66 with two).
-template <typename T, typename S, int D>
-static cudaError_t launch_typed(const TreeArgs& a, const TreeWs& w, cudaStream_t st) {
-  if constexpr (sizeof(S) == 4 && D == 128) {
-    const long long tiles =
-        (long long)a.B * a.Hkv * ((a.N / SAS_BLOCK + SC_ROWS - 1) / SC_ROWS);
-    if (tiles > 148) return launch_step<T, S, D, 64>(a, w, st);
-  }
-  return launch_step<T, S, D, D>(a, w, st);
 }
 
 cudaError_t launch_tree_scores(const TreeArgs& a, const TreeWs& w, int bf16, int sum_bf16, int d,
