@@ -86,13 +86,17 @@ __device__ __forceinline__ bool beats(float sa, int ia, float sb, int ib) {
 }
 
 // ---------------------------------------------------------------- Top-K lists
+// Order-preserving map of a score to an unsigned integer: a larger score has a
+// larger image. A -0 must be stored as +0 beforehand so that exact ties are equal.
+__device__ __forceinline__ uint32_t order_bits(float s) {
+  const uint32_t u = __float_as_uint(s);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
 // Order key of a candidate block: larger score first, then lower block index,
 // packed into one unsigned 64-bit integer (larger key = better candidate).
-// A -0 score must be stored as +0 beforehand so that exact ties are equal.
 __device__ __forceinline__ unsigned long long cand_key(float s, int m) {
-  uint32_t u = __float_as_uint(s);
-  u = (u & 0x80000000u) ? ~u : (u | 0x80000000u);  // order-preserving map
-  return ((unsigned long long)u << 32) | (0xffffffffu - (uint32_t)m);
+  return ((unsigned long long)order_bits(s) << 32) | (0xffffffffu - (uint32_t)m);
 }
 
 __device__ __forceinline__ float key_score(unsigned long long key) {

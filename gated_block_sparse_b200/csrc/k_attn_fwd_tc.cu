@@ -73,39 +73,6 @@ enum Bar {
 };
 static_assert(NBAR * 8 + 4 <= 128, "barriers and the TMEM address fit their 128 bytes");
 
-// (a0, a1) = (x0, x1) * c + (o, o) as one packed fp32x2 FMA
-__device__ __forceinline__ void fma2c(float& a0, float& a1, float x0, float x1, float c, float o) {
-  asm("{\n\t.reg .b64 x, c, o, a;\n\t"
-      "mov.b64 x, {%2, %3};\n\t"
-      "mov.b64 c, {%4, %4};\n\t"
-      "mov.b64 o, {%5, %5};\n\t"
-      "fma.rn.f32x2 a, x, c, o;\n\t"
-      "mov.b64 {%0, %1}, a;\n\t}"
-      : "=f"(a0), "=f"(a1)
-      : "f"(x0), "f"(x1), "f"(c), "f"(o));
-}
-// (s0, s1) += (x0, x1) as one packed fp32x2 add
-__device__ __forceinline__ void add2(float& s0, float& s1, float x0, float x1) {
-  asm("{\n\t.reg .b64 s, x;\n\t"
-      "mov.b64 s, {%0, %1};\n\t"
-      "mov.b64 x, {%2, %3};\n\t"
-      "add.rn.f32x2 s, s, x;\n\t"
-      "mov.b64 {%0, %1}, s;\n\t}"
-      : "+f"(s0), "+f"(s1)
-      : "f"(x0), "f"(x1));
-}
-
-// O += P V with the A operand (P, bf16, 128 lanes x 16 elements packed two
-// per 32-bit column) read from TMEM and B from shared memory.
-__device__ __forceinline__ void mma_bf16_tmem_a(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc,
-                                                uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
-      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
 // 32 lanes x 32 consecutive 32-bit columns from registers (lane of the warp's
 // quarter, columns taddr.col .. +31)
 __device__ __forceinline__ void tmem_st32u(uint32_t taddr, const uint32_t (&v)[32]) {
@@ -119,13 +86,6 @@ __device__ __forceinline__ void tmem_st32u(uint32_t taddr, const uint32_t (&v)[3
       "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
       "r"(v[29]), "r"(v[30]), "r"(v[31])
       : "memory");
-}
-
-// max(a, b, c) in one instruction
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
 }
 
 }  // namespace
@@ -262,7 +222,7 @@ __global__ void __launch_bounds__(FT_THREADS, 2) k_attn_fwd_tc(
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {  // P_j: columns 8 ks .. 8 ks + 7 of S_j's buffer
           const uint64_t bd = tc::sw128_desc(v_addr + ks * 2048, 8192, 1024);
-          mma_bf16_tmem_a(tm_o, tm_s[j & 1] + 8 * ks, bd, ID_PV, (j > 0 || ks > 0) ? 1u : 0u);
+          tc::mma_bf16_tmem_a(tm_o, tm_s[j & 1] + 8 * ks, bd, ID_PV, (j > 0 || ks > 0) ? 1u : 0u);
         }
         tc::commit(&bars[B_OD]);
         tc::commit(&bars[B_VE + (j & 1)]);
@@ -343,9 +303,9 @@ __global__ void __launch_bounds__(FT_THREADS, 2) k_attn_fwd_tc(
 #pragma unroll
       for (int i = 8; i < 64; i += 8) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) zm[c] = max3(zm[c], z[i + 2 * c], z[i + 2 * c + 1]);
+        for (int c = 0; c < 4; ++c) zm[c] = tc::max3(zm[c], z[i + 2 * c], z[i + 2 * c + 1]);
       }
-      const float mx = max3(zm[0], zm[1], fmaxf(zm[2], zm[3])) * c1 + bias;
+      const float mx = tc::max3(zm[0], zm[1], fmaxf(zm[2], zm[3])) * c1 + bias;
       const float mnew = fmaxf(m, mx);
       const bool grow = (j == 0) || (mnew > m + RESCALE_LOG2);
       const float muse = grow ? mnew : m;
@@ -355,9 +315,9 @@ __global__ void __launch_bounds__(FT_THREADS, 2) k_attn_fwd_tc(
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
         float a0, a1;
-        fma2c(a0, a1, z[2 * i], z[2 * i + 1], c1, off);
+        tc::fma2c(a0, a1, z[2 * i], z[2 * i + 1], c1, off);
         const float p0 = tc::ex2(a0), p1 = tc::ex2(a1);
-        add2(rs0, rs1, p0, p1);
+        tc::add2(rs0, rs1, p0, p1);
         __nv_bfloat162 h2 = __floats2bfloat162_rn(p0, p1);
         pk[i] = *reinterpret_cast<uint32_t*>(&h2);
       }

@@ -31,13 +31,6 @@ __device__ uint32_t g_tokens_err = 0;
 constexpr int TOK_CMAX = 512;  // history blocks of a query block at most
 
 // ------------------------------------------------------------------ selection
-// Order-preserving unsigned key of a score: a larger score has a larger key,
-// and -0 was mapped to +0 before, so equal scores have equal keys.
-__device__ __forceinline__ uint32_t score_key(float x) {
-  const uint32_t u = __float_as_uint(x);
-  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
-}
-
 // One warp: the gate and the Top-K of one row's C scores si[0 .. C) (C <= 32
 // KPL). kk = min(topk, C) blocks are kept, ordered by (score desc, block
 // asc): tau, the kk-th largest key, is found bit by bit (the largest value
@@ -58,7 +51,7 @@ __device__ __forceinline__ void select_row(const float* si, int C, int kk, int t
   for (int j = 0; j < KPL; ++j) {
     const int m = j * 32 + lane;
     sv[j] = m < C ? si[m] : -FLT_MAX;
-    kv[j] = m < C ? score_key(sv[j]) : 0u;
+    kv[j] = m < C ? order_bits(sv[j]) : 0u;
     mx = fmaxf(mx, sv[j]);
   }
   mx = warp_max(mx);

@@ -68,44 +68,6 @@ enum Bar {
 };
 static_assert(NBAR * 8 + 4 <= 128, "barriers and the TMEM address fit their 128 bytes");
 
-// O += P V with P (bf16, two per 32-bit column) read from TMEM.
-__device__ __forceinline__ void mma_tmem_a(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc,
-                                           uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
-      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// (a0, a1) = (x0, x1) * c + (o, o) as one packed fp32x2 FMA
-__device__ __forceinline__ void fma2c(float& a0, float& a1, float x0, float x1, float c, float o) {
-  asm("{\n\t.reg .b64 x, c, o, a;\n\t"
-      "mov.b64 x, {%2, %3};\n\t"
-      "mov.b64 c, {%4, %4};\n\t"
-      "mov.b64 o, {%5, %5};\n\t"
-      "fma.rn.f32x2 a, x, c, o;\n\t"
-      "mov.b64 {%0, %1}, a;\n\t}"
-      : "=f"(a0), "=f"(a1)
-      : "f"(x0), "f"(x1), "f"(c), "f"(o));
-}
-// (s0, s1) += (x0, x1) as one packed fp32x2 add
-__device__ __forceinline__ void add2(float& s0, float& s1, float x0, float x1) {
-  asm("{\n\t.reg .b64 s, x;\n\t"
-      "mov.b64 s, {%0, %1};\n\t"
-      "mov.b64 x, {%2, %3};\n\t"
-      "add.rn.f32x2 s, s, x;\n\t"
-      "mov.b64 {%0, %1}, s;\n\t}"
-      : "+f"(s0), "+f"(s1)
-      : "f"(x0), "f"(x1));
-}
-// max(a, b, c) in one instruction
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
 // Barrier 1 over the softmax and MMA warps (the TMA warp is not in it).
 __device__ __forceinline__ void sync_but_tma() {
   asm volatile("bar.sync 1, %0;" ::"n"(TT_THREADS - 32) : "memory");
@@ -403,8 +365,8 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
         const uint64_t vd = v_desc + (((j & 1) * 2 * L::TILE) >> 4);
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {  // P_j: its upper part, then its lower, 8 columns a step
-          mma_tmem_a(tm_o, tm_s[j & 1] + 8 * ks, vd + (((ks & 3) * 2048) >> 4), ID_PV,
-                     (j > 0 || ks > 0) ? 1u : 0u);
+          tc::mma_bf16_tmem_a(tm_o, tm_s[j & 1] + 8 * ks, vd + (((ks & 3) * 2048) >> 4),
+                              ID_PV, (j > 0 || ks > 0) ? 1u : 0u);
         }
         tc::commit(&bars[B_OD]);
         tc::commit(&bars[B_VE + (j & 1)]);
@@ -493,7 +455,7 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
 #pragma unroll
       for (int i = 8; i < NC; i += 8) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) zm[c] = max3(zm[c], z[i + 2 * c], z[i + 2 * c + 1]);
+        for (int c = 0; c < 4; ++c) zm[c] = tc::max3(zm[c], z[i + 2 * c], z[i + 2 * c + 1]);
       }
       // c1 > 0, so the maximum of z c1 + bias is that of z
       const float mx =
@@ -507,9 +469,9 @@ __global__ void __launch_bounds__(TT_THREADS, 2)
 #pragma unroll
       for (int i = 0; i < NC / 2; ++i) {
         float a0, a1;
-        fma2c(a0, a1, z[2 * i], z[2 * i + 1], c1, off);
+        tc::fma2c(a0, a1, z[2 * i], z[2 * i + 1], c1, off);
         const float p0 = tc::ex2(a0), p1 = tc::ex2(a1);
-        add2(r0, r1, p0, p1);
+        tc::add2(r0, r1, p0, p1);
         const uint32_t w0 = __float_as_uint(p0), w1 = __float_as_uint(p1);
         pk[0][i] = __byte_perm(w0, w1, 0x7632);
         const __nv_bfloat162 h2 = __floats2bfloat162_rn(p0 - __uint_as_float(w0 & 0xffff0000u),

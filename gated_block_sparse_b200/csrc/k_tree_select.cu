@@ -280,8 +280,7 @@ __global__ void __launch_bounds__(THREADS) k_tree_select(TreeArgs a, TreeWs w) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         if (m + k < Ci && !(bucket(v[k]) < bound) && at < SEL_LIST)
-          list[at++] = ((unsigned long long)score_key(v[k]) << 32) |
-                       (0xffffffffu - (uint32_t)(m + k));
+          list[at++] = cand_key(v[k] + 0.f, m + k);
       }
     }
   }

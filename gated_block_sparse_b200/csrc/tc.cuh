@@ -92,6 +92,18 @@ __device__ __forceinline__ void mma_bf16(uint32_t tmem_d, uint64_t adesc, uint64
       : "memory");
 }
 
+// mma_bf16 with the A operand (128 lanes x 16 elements packed two per 32-bit
+// column) read from TMEM.
+__device__ __forceinline__ void mma_bf16_tmem_a(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc,
+                                                uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // Arrive once on `bar` when every tcgen05 operation issued so far by this
 // thread has completed.
 __device__ __forceinline__ void commit(uint64_t* bar) {
@@ -172,6 +184,34 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// (a0, a1) = (x0, x1) * c + (o, o) as one packed fp32x2 FMA
+__device__ __forceinline__ void fma2c(float& a0, float& a1, float x0, float x1, float c, float o) {
+  asm("{\n\t.reg .b64 x, c, o, a;\n\t"
+      "mov.b64 x, {%2, %3};\n\t"
+      "mov.b64 c, {%4, %4};\n\t"
+      "mov.b64 o, {%5, %5};\n\t"
+      "fma.rn.f32x2 a, x, c, o;\n\t"
+      "mov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(a0), "=f"(a1)
+      : "f"(x0), "f"(x1), "f"(c), "f"(o));
+}
+// (s0, s1) += (x0, x1) as one packed fp32x2 add
+__device__ __forceinline__ void add2(float& s0, float& s1, float x0, float x1) {
+  asm("{\n\t.reg .b64 s, x;\n\t"
+      "mov.b64 s, {%0, %1};\n\t"
+      "mov.b64 x, {%2, %3};\n\t"
+      "add.rn.f32x2 s, s, x;\n\t"
+      "mov.b64 {%0, %1}, s;\n\t}"
+      : "+f"(s0), "+f"(s1)
+      : "f"(x0), "f"(x1));
+}
+// max(a, b, c) in one instruction
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 // Vector reduction-add of four fp32 values into global memory (16-byte aligned).

@@ -119,15 +119,8 @@ __device__ __forceinline__ size_t tree_block_row(const TreeArgs& a, int b, int r
   return ((size_t)b * a.Hkv + r) * a.N + (size_t)place * SAS_BLOCK;
 }
 
-// order-preserving map of a score to an unsigned integer (-0 becomes +0, so
-// that exact ties are equal keys)
-__device__ __forceinline__ uint32_t score_key(float s) {
-  const uint32_t u = __float_as_uint(s + 0.f);
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-__device__ __forceinline__ float score_of(uint32_t key) {
-  return __uint_as_float((key & 0x80000000u) ? (key & 0x7fffffffu) : ~key);
-}
+// Order bits of a score of either zero (exact ties are equal).
+__device__ __forceinline__ uint32_t score_key(float s) { return order_bits(s + 0.f); }
 
 // What selection leaves of a row (sequence, kv group, drafted token): with
 // the scores themselves it says which blocks the row keeps and their gates,
