@@ -216,7 +216,8 @@ __device__ __noinline__ float2 repair_row(const TreeArgs& a, const TreeWs& w, co
 template <int D, int COPIES>
 __global__ void __launch_bounds__(TT_THREADS, 2)
     k_tree_attn_tc(const __grid_constant__ CUtensorMap kmap,
-                   const __grid_constant__ CUtensorMap vmap, TreeArgs a, TreeWs w) {
+                   const __grid_constant__ CUtensorMap vmap, const __grid_constant__ TreeArgs a,
+                   const __grid_constant__ TreeWs w) {
   using L = Lay<D>;
   constexpr int PC = D / 8;  // 16-byte pieces of a row
   constexpr int RT = 128 / COPIES, NC = 64 / COPIES;  // rows of a copy, keys of a thread

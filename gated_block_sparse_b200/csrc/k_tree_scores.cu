@@ -86,13 +86,15 @@ template <> struct Raw8<__nv_bfloat16> {
   __device__ __forceinline__ void parts(uint4 (&out)[1]) const { out[0] = a; }
 };
 
+__host__ __device__ __forceinline__ int scores_cols(int T) { return (T + 15) & ~15; }
+
 // The score of one (summary, token) by fp32 FMAs, for one that the split products
 // made inf or NaN: a part of an infinity is NaN (inf - inf), as is its product
 // with a part that is 0, and a finite value past the largest bf16 rounds to an
 // infinite part. The mean query is the sum of its three parts in shared memory
 // (its first part alone where that is not finite).
 template <typename S, int D>
-__device__ __noinline__ float score_by_fma(const S* sum, const unsigned char* sb, int row, int NT) {
+__device__ __forceinline__ float score_by_fma(const S* sum, const unsigned char* sb, int row, int NT) {
   float dot = 0.f;
 #pragma unroll 2
   for (int p = 0; p < D / 8; ++p) {
@@ -114,17 +116,36 @@ __device__ __noinline__ float score_by_fma(const S* sum, const unsigned char* sb
   return dot;
 }
 
+// The scores of block m and the tokens t0 + i, i in `again`, which the MMAs left
+// inf or NaN: by FMAs, or -inf where the block's page lies outside the pool.
+template <typename S, int D>
+__device__ __noinline__ void scores_again(const TreeArgs& a, float* scores, int b, int r, int m,
+                                          int t0, uint32_t again, const unsigned char* sb) {
+  const int C = a.N / SAS_BLOCK, place = tree_place(a, b, m, &g_tree_scores_err);
+  const size_t group = (size_t)b * a.Hkv + r;
+  const size_t row = a.table ? (size_t)max(place, 0) * a.Hkv + r : group * C + m;
+  float* out = scores + (group * a.T + t0) * tree_stride(C) + m;
+  for (; again; again &= again - 1) {
+    const int t = __ffs(again) - 1;
+    const float dot = score_by_fma<S, D>(static_cast<const S*>(a.ksum) + row * D, sb, t0 + t,
+                                         scores_cols(a.T));
+    out[(size_t)t * tree_stride(C)] = place < 0 ? -INFINITY : dot * a.scale + 0.f;
+  }
+}
+
 // CTAs an SM: the 64 fp32 values that a thread loads ahead with D = 128 need
 // more than the 128 registers of two (a spilled one would be waited for).
 template <typename S, int D>
 constexpr int scores_ctas() { return sizeof(S) * D > 256 ? 1 : 2; }
 
-__host__ __device__ __forceinline__ int scores_cols(int T) { return (T + 15) & ~15; }
-
 }  // namespace
 
+// The arguments are grid constants, here and in the attention: a function that
+// takes them by reference would have every thread copy them to its stack.
 template <typename T, typename S, int D>
-__global__ void __launch_bounds__(SC_THREADS, scores_ctas<S, D>()) k_tree_scores(TreeArgs a, TreeWs w, int stretch) {
+__global__ void __launch_bounds__(SC_THREADS, scores_ctas<S, D>())
+    k_tree_scores(const __grid_constant__ TreeArgs a, const __grid_constant__ TreeWs w,
+                  int stretch) {
   constexpr int NP = sizeof(S) == 4 ? 3 : 1;     // parts of a summary
   constexpr int PC = D / 8;                      // 16-byte pieces of a bf16 row
   constexpr int PER = SC_ROWS * PC / SC_THREADS; // pieces of a tile of a thread
@@ -294,16 +315,7 @@ __global__ void __launch_bounds__(SC_THREADS, scores_ctas<S, D>()) k_tree_scores
           o += CS;
         }
       }
-      if (again) {
-        const int place = tree_place(a, b, m, err);
-        const S* sum = static_cast<const S*>(a.ksum) + (place < 0 ? 0 : sum_row(place) * D);
-        do {
-          const int t = __ffs(again) - 1;
-          again &= again - 1;
-          out[(size_t)(t0 + t) * CS + m] =
-              place < 0 ? -INFINITY : score_by_fma<S, D>(sum, sb, t0 + t, NT) * a.scale + 0.f;
-        } while (again);
-      }
+      if (again) scores_again<S, D>(a, w.scores, b, r, m, t0, again, sb);
     }
   }
   tc::fence_before_sync();
