@@ -20,7 +20,7 @@ def inv_freq(rot: int, base: float = 10000.0, scaling: str = "none", factor: flo
       none    as trained;
       linear  every frequency divided by factor (positions interpolated);
       base    the base raised to base * factor^(rot/(rot-2)): the fastest pair
-              is kept, the slowest slowed by factor;
+              is kept, the slowest slowed by factor (one pair, rot 2, is kept);
       parts   pairs that turn fewer than `slow` times over the trained length
               are slowed by factor, those above `fast` turns kept, a linear
               ramp over the turns between; amplitude 1 + 0.1 ln factor for
@@ -29,8 +29,8 @@ def inv_freq(rot: int, base: float = 10000.0, scaling: str = "none", factor: flo
     """
     if rot < 2 or rot % 2:
         raise ValueError(f"rot must be even and at least 2 (got {rot})")
-    if not base > 0 or not factor >= 1:
-        raise ValueError(f"base must be positive and factor at least 1 (got {base}, {factor})")
+    if not 0 < base < math.inf or not 1 <= factor < math.inf:
+        raise ValueError(f"base must be positive, factor at least 1, both finite (got {base}, {factor})")
     amplitude = 1.0
     p = torch.arange(rot // 2, dtype=torch.float64) * 2.0 / rot
     if scaling == "base" and rot > 2:
@@ -39,8 +39,9 @@ def inv_freq(rot: int, base: float = 10000.0, scaling: str = "none", factor: flo
     if scaling == "linear":
         f = f / factor
     elif scaling == "parts":
-        if not fast > slow:
-            raise ValueError(f"fast must be above slow (got {fast}, {slow})")
+        if not -math.inf < slow < fast < math.inf or not 0 < trained < math.inf:
+            raise ValueError(f"fast must be above slow, both finite, and trained positive "
+                             f"(got {fast}, {slow}, {trained})")
         turns = trained * f / (2.0 * math.pi)
         keep = ((turns - slow) / (fast - slow)).clamp(0.0, 1.0)
         f = f * keep + f / factor * (1.0 - keep)

@@ -222,7 +222,12 @@ def test_inverse_frequencies():
     assert (parts <= f).all() and (parts * 16 >= f * (1 - 1e-6)).all()
     assert abs(amp - (1 + 0.1 * np.log(16.0))) < 1e-12
     for bad in (dict(rot=7), dict(rot=0), dict(rot=8, factor=0.5), dict(rot=8, base=0.0),
-                dict(rot=8, scaling="other"), dict(rot=8, scaling="parts", slow=2.0, fast=1.0)):
+                dict(rot=8, scaling="other"), dict(rot=8, scaling="parts", slow=2.0, fast=1.0),
+                dict(rot=8, base=float("inf")), dict(rot=8, base=float("nan")),
+                dict(rot=8, scaling="linear", factor=float("inf")),
+                dict(rot=8, scaling="parts", factor=2.0, trained=0),
+                dict(rot=8, scaling="parts", factor=2.0, trained=float("nan")),
+                dict(rot=8, scaling="parts", factor=2.0, fast=float("inf"))):
         with pytest.raises(ValueError):
             rope.inv_freq(**bad)
 
