@@ -699,7 +699,7 @@ sas_status sas_device_status(int clear, sas_stream_t stream) {
       msg += w.kernel;
       if (v & sas::kErrWaitTimeout) msg += ": a bounded wait gave up";
       if (v & sas::kErrBadIndex) msg += (v & sas::kErrWaitTimeout) ? ", " : ": ";
-      if (v & sas::kErrBadIndex) msg += "a selection index out of range was replaced";
+      if (v & sas::kErrBadIndex) msg += "an index out of range was replaced or left out";
     }
     all |= v;
     if (clear && v) {

@@ -371,7 +371,10 @@ cudaError_t launch_tree_attn_simt(const TreeArgs& a, const TreeWs& w, int d, cud
 // 20.1 us a call, 22.2 with 32 splits, 22.0 with 8), or 24 of the fp32 kernel,
 // whose units take longer (20 tokens over 46 blocks: 51 us with 24 splits, 62
 // with 20). Even two units are split: a unit of one CTA costs as much as the
-// join.
+// join. The cap was set where units are few; a call with one kv head and many
+// selected units would use the 32 splits that the join takes at most (one
+// sequence of 128K, 64 tokens, top-k 127: 37.0 us with 32, 44.1 as it is; top-k
+// 63 31.1 and 33.2; 4 tokens, top-k 15 18.3 and 18.5).
 int tree_splits(int B, int Hq, int Hkv, int T, int N, int topk, int bf16) {
   const int tile = bf16 ? 128 : TA_ROWS;
   const long long tiles = ((long long)(Hq / Hkv) * T + tile - 1) / tile;

@@ -457,7 +457,7 @@ def sas_select_bwd(q, ksum, Hkv: int, idx, cnt, dlogg, dq, dk, scale: float = 0.
 
 
 def sas_device_status(clear: bool = False, stream=None) -> tuple[int, str]:
-    """Synchronise `stream` and read the kernels' device error words.
+    """Synchronise `stream` and read the current device's error words of the kernels.
 
     Returns (status, message): SAS_ERR_TIMEOUT (4) if a bounded wait gave up,
     SAS_ERR_INTERNAL (5) if a selection index was out of range, 0 otherwise.

@@ -108,8 +108,10 @@ sas_status sas_page_map(const int32_t* lens, const int32_t* nnew, int32_t* block
  *     -1 leaves the token out);
  *   when the last row of a 64-token block is written and ksum is given, the
  *   mean of the block's 64 stored keys goes to ksum [B][Hkv][N/64][d], or
- *   [npages][Hkv][d], of type sum_dt (as sas_block_summary computes it; a
- *   block with a token left out keeps its summary);
+ *   [npages][Hkv][d], of type sum_dt (summed in fp32 and rounded once, as
+ *   sas_block_summary does, but in another order, which also depends on types
+ *   and strides: the last bits may differ; a block with a token left out in
+ *   this call keeps its summary);
  *   q [B][Hq][T][d], when given, is rotated at the same positions into
  *   qo [B][Hq][T][d] (contiguous), all its rows.
  *   k, v [B][Hkv][T][d] and q are read through element strides {batch, head,
@@ -137,7 +139,9 @@ sas_status sas_cache_append(const void* q, const int64_t* q_strides, void* qo, c
  * path, for several query tokens a sequence). Drafted token i of sequence b
  * has parent parents[b][i] < i (-1: the last cached token), depth = number of
  * ancestors, position lens[b] + depth, and gets what sas_decode gives on a
- * cache with the path from the root to it appended: its own Top-K row over
+ * cache with the path from the root to it appended, up to the rounding of fp32
+ * sums in another order (scores that nearly tie may select another block): its
+ * own Top-K row over
  * the (lens[b] + depth)/64 history blocks, gate, and attention over the kept
  * blocks, the current block's tokens and its ancestors. Where a path fills the
  * block of the cache's tail, that block is history for the tokens past it,
