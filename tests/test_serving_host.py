@@ -67,7 +67,6 @@ def stride(*s):
     ("sas_rotary", ROTARY, dict(inverse=3), 1, b"inverse"),
     ("sas_rotary", ROTARY, dict(pos=FAKE, start=FAKE), 1, b"excludes"),
     ("sas_rotary", ROTARY, dict(start=FAKE + 4), 1, b"start"),
-    ("sas_rotary", ROTARY, dict(parents=FAKE, N=1025), 2, b"1024 with parents"),
     ("sas_rotary", ROTARY, dict(B=70000), 2, b"65535"),
     ("sas_rotary", ROTARY, dict(qs=stride(0, -128, 128)), 1, b"input strides"),
     ("sas_rotary", ROTARY, dict(kos=stride(2048, 1024, 64)), 1, b"output strides"),
@@ -90,8 +89,6 @@ def stride(*s):
     ("sas_cache_append", APPEND, dict(lens=None), 1, b"lens"),
     ("sas_cache_append", APPEND, dict(vs=stride(1, -1, 1)), 1, b"input strides"),
     ("sas_cache_append", APPEND, dict(kc=FAKE + 2), 1, b"kc"),
-    ("sas_cache_append", APPEND, dict(T=(1 << 30) + 1, ks=stride(0, 128, 0), vs=stride(0, 128, 0)),
-     2, b"2^30"),
     ("sas_decode_tree", TREE, dict(T=65), 2, b"64 drafted"),
     ("sas_decode_tree", TREE, dict(T=0), 1, b"T must be"),
     ("sas_decode_tree", TREE, dict(N=100), 1, b"multiple of 64"),
@@ -111,6 +108,15 @@ def stride(*s):
 def test_refusals(lib, fn, base, change, status, text):
     st = getattr(lib, fn)(*{**base, **change}.values())
     assert st == status and text in lib.sas_last_error_message(), lib.sas_last_error_message()
+
+
+@pytest.mark.parametrize("fn,base,change,status,text", [
+    ("sas_rotary", ROTARY, dict(parents=FAKE, N=1025), 2, b"1024 with parents"),
+    ("sas_cache_append", APPEND, dict(T=(1 << 30) + 1, ks=stride(0, 128, 0), vs=stride(0, 128, 0)),
+     2, b"2^30"),
+])
+def test_refusals_of_sizes(lib, fn, base, change, status, text):
+    test_refusals(lib, fn, base, change, status, text)
 
 
 @pytest.mark.parametrize("change,text", [
@@ -222,14 +228,20 @@ def test_inverse_frequencies():
     assert (parts <= f).all() and (parts * 16 >= f * (1 - 1e-6)).all()
     assert abs(amp - (1 + 0.1 * np.log(16.0))) < 1e-12
     for bad in (dict(rot=7), dict(rot=0), dict(rot=8, factor=0.5), dict(rot=8, base=0.0),
-                dict(rot=8, scaling="other"), dict(rot=8, scaling="parts", slow=2.0, fast=1.0),
-                dict(rot=8, base=float("inf")), dict(rot=8, base=float("nan")),
-                dict(rot=8, scaling="linear", factor=float("inf")),
-                dict(rot=8, scaling="parts", factor=2.0, trained=0),
-                dict(rot=8, scaling="parts", factor=2.0, trained=float("nan")),
-                dict(rot=8, scaling="parts", factor=2.0, fast=float("inf"))):
+                dict(rot=8, scaling="other"), dict(rot=8, scaling="parts", slow=2.0, fast=1.0)):
         with pytest.raises(ValueError):
             rope.inv_freq(**bad)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(base=float("inf")), dict(base=float("nan")),
+    dict(scaling="linear", factor=float("inf")),
+    dict(scaling="parts", factor=2.0, trained=0),
+    dict(scaling="parts", factor=2.0, trained=float("nan")),
+    dict(scaling="parts", factor=2.0, fast=float("inf"))])
+def test_inverse_frequencies_refuse_what_is_not_finite(bad):
+    with pytest.raises(ValueError):
+        rope.inv_freq(8, **bad)
 
 
 @pytest.mark.parametrize("inter", [False, True])
